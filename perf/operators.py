@@ -14,7 +14,7 @@ Four operators:
 Pool layout: uint8 ``[L, N, H_kv, B * D / 2 + B * D / 16]``; a (block, head)
 chunk holds D / 32 code planes ``[B][16 bytes]`` (value 2i of a group in the
 low nibble of byte i, 2i + 1 in the high one, code c as c + 8), then the fp16
-scales ``[B][D / 32]``.
+scales, ``[B][D / 32]`` in the K pool and ``[D / 32][B]`` in the V pool.
 """
 
 import math
@@ -153,12 +153,13 @@ def _nibbles(code):
     return code[..., 0::2] | (code[..., 1::2] << 4)
 
 
-def _parts(pool, B, D):
+def _parts(pool, B, D, name):
     """Views of a pool [L, N, H, chunk]: codes [L, N, H, D/32, B, 16], scales [L, N, H, B, D/32]."""
-    L, N, H, _ = pool.shape
     codes = pool[..., : B * D // 2].unflatten(-1, (D // 32, B, 16))
-    scales = pool[..., B * D // 2 :].view(torch.float16).unflatten(-1, (B, D // 32))
-    return codes, scales
+    scales = pool[..., B * D // 2 :].view(torch.float16)
+    if name == "k":
+        return codes, scales.unflatten(-1, (B, D // 32))
+    return codes, scales.unflatten(-1, (D // 32, B)).transpose(-1, -2)
 
 
 def _values(codes, scales):
@@ -167,10 +168,10 @@ def _values(codes, scales):
     return (c.float() - 8) * scales.float().unsqueeze(-1)
 
 
-def _fill(N, B, H, D, g):
+def _fill(N, B, H, D, g, name):
     """A pool of one layer holding quantized N(0, 1) rows."""
     pool = torch.empty(1, N, H, B * D // 2 + B * D // 16, dtype=torch.uint8, device=DEV)
-    codes, scales = _parts(pool, B, D)
+    codes, scales = _parts(pool, B, D, name)
     for a in range(0, N, 2048):
         b = min(N, a + 2048)
         x = torch.randn(b - a, H, D // 32, B, 32, device=DEV, generator=g).bfloat16().float()
@@ -220,7 +221,7 @@ def _prep_decode(case, g, r):
     perm = r.permutation(N).astype(np.int32)
     table, lens = _batch(case, perm)
     n, mb = table.shape
-    s = dict(case=case, k_pool=_fill(N, B, H, D, g), v_pool=_fill(N, B, H, D, g), q=_bf16(g, n, H * G, D),
+    s = dict(case=case, k_pool=_fill(N, B, H, D, g, "k"), v_pool=_fill(N, B, H, D, g, "v"), q=_bf16(g, n, H * G, D),
              table=torch.from_numpy(table).to(DEV), lens=torch.from_numpy(lens).to(DEV), n=n, mb=mb,
              out=torch.empty(n, H * G, D, dtype=torch.bfloat16, device=DEV))
     if own:
@@ -253,7 +254,8 @@ def _prep_prefill(case, g, r):
         at += k
     start = np.concatenate([[0], np.cumsum(chunk)]).astype(np.int32)
     lens = (np.array(hist) + np.array(chunk)).astype(np.int32)
-    s = dict(case=case, k_pool=_fill(N, B, H, D, g), v_pool=_fill(N, B, H, D, g), q=_bf16(g, int(start[-1]), H * G, D),
+    s = dict(case=case, k_pool=_fill(N, B, H, D, g, "k"), v_pool=_fill(N, B, H, D, g, "v"),
+             q=_bf16(g, int(start[-1]), H * G, D),
              table=torch.from_numpy(table).to(DEV), lens=torch.from_numpy(lens).to(DEV), n=n, mb=mb,
              start=torch.from_numpy(start).to(DEV), max_chunk=max(chunk),
              out=torch.empty(int(start[-1]), H * G, D, dtype=torch.bfloat16, device=DEV))
@@ -347,7 +349,7 @@ def _plain_write(s):
     blk, o = s["slots"] // B, s["slots"] % B
     out = {}
     for name in ("k", "v"):
-        codes, scales = _parts(s[name + "_pool"], B, D)
+        codes, scales = _parts(s[name + "_pool"], B, D, name)
         q, d = _quantize(s[name].float().unflatten(-1, (D // 32, 32)))  # [L, n, H, D/32, 32], [L, n, H, D/32]
         codes[:, blk, :, :, o] = _nibbles(q).transpose(0, 1)
         scales[:, blk, :, o] = d.transpose(0, 1)
@@ -356,40 +358,40 @@ def _plain_write(s):
     return out
 
 
-def _rows(pool, table, B, D):
+def _rows(s, name):
     """The listed sequences' rows as float32 [n, H, max_blocks * B, D]."""
-    codes, scales = _parts(pool, B, D)
-    at = table.long().clamp(min=0)
+    codes, scales = _parts(s[name + "_pool"], s["case"]["B"], s["case"]["D"], name)
+    at = s["table"].long().clamp(min=0)
     x = _values(codes[0][at], scales[0][at].transpose(-1, -2))  # [n, mb, H, D/32, B, 32]
     return x.permute(0, 2, 1, 4, 3, 5).flatten(4).flatten(2, 3)
 
 
 def _plain_decode(s):
     c = s["case"]
-    B, H, G, D = c["B"], c["H"], c["G"], c["D"]
+    H, G, D = c["H"], c["G"], c["D"]
     q = s["q"].float().unflatten(1, (H, G))
-    x = torch.matmul(q, _rows(s["k_pool"], s["table"], B, D).transpose(-1, -2)) / math.sqrt(D)
+    x = torch.matmul(q, _rows(s, "k").transpose(-1, -2)) / math.sqrt(D)
     past = torch.arange(x.shape[-1], device=DEV) >= s["lens"][:, None, None, None]
     x = x.masked_fill(past, -math.inf)
     p = torch.exp(x - x.amax(-1, keepdim=True))
-    o = torch.matmul(p, _rows(s["v_pool"], s["table"], B, D)) / p.sum(-1, keepdim=True)
+    o = torch.matmul(p, _rows(s, "v")) / p.sum(-1, keepdim=True)
     return o.flatten(1, 2).bfloat16()
 
 
 def _plain_prefill(s):
     c = s["case"]
-    B, H, G, D, n, C = c["B"], c["H"], c["G"], c["D"], s["n"], s["max_chunk"]
+    H, G, D, C = c["H"], c["G"], c["D"], s["max_chunk"]
     start, lens = s["start"].long(), s["lens"].long()
     cnt = start[1:] - start[:-1]
     i = torch.arange(C, device=DEV)
     row = (start[:-1, None] + i).clamp(max=s["q"].shape[0] - 1)
     q = s["q"].float()[row].unflatten(2, (H, G)).permute(0, 2, 3, 1, 4).flatten(2, 3)  # [n, H, G * C, D]
-    x = torch.matmul(q, _rows(s["k_pool"], s["table"], B, D).transpose(-1, -2)) / math.sqrt(D)
+    x = torch.matmul(q, _rows(s, "k").transpose(-1, -2)) / math.sqrt(D)
     pos = (lens - cnt)[:, None] + i  # [n, C]
     past = torch.arange(x.shape[-1], device=DEV) > pos[:, None, None, :, None]
     x = x.unflatten(2, (G, C)).masked_fill(past, -math.inf).flatten(2, 3)
     p = torch.exp(x - x.amax(-1, keepdim=True))
-    o = torch.matmul(p, _rows(s["v_pool"], s["table"], B, D)) / p.sum(-1, keepdim=True)
+    o = torch.matmul(p, _rows(s, "v")) / p.sum(-1, keepdim=True)
     o = o.unflatten(2, (G, C)).permute(0, 3, 1, 2, 4).flatten(2, 3)  # [n, C, Hq, D]
     t = torch.arange(s["q"].shape[0], device=DEV)
     seq = torch.searchsorted(start[1:], t, right=True)
@@ -488,11 +490,12 @@ def _exact_write(s):
     return out
 
 
-def _exact_rows(pool, ids, h, length, B, D):
+def _exact_rows(s, name, ids, h, length, B, D):
     """float64 [length, D] of one sequence and head, through the chunk's bytes."""
-    chunk = pool[0, ids.long(), h]  # [nb, bytes]
+    chunk = s[name + "_pool"][0, ids.long(), h]  # [nb, bytes]
     code = chunk[:, : B * D // 2].reshape(-1, D // 32, B, 16).permute(0, 2, 1, 3)  # [nb, B, D/32, 16]
-    d = chunk[:, B * D // 2 :].contiguous().view(torch.float16).reshape(-1, B, D // 32).double()
+    d = chunk[:, B * D // 2 :].contiguous().view(torch.float16).double()
+    d = d.reshape(-1, B, D // 32) if name == "k" else d.reshape(-1, D // 32, B).permute(0, 2, 1)
     lo, hi = (code % 16).double() - 8.0, (code // 16).double() - 8.0
     x = torch.empty(*code.shape[:3], 32, dtype=torch.float64, device=DEV)
     x[..., 0::2], x[..., 1::2] = lo * d[..., None], hi * d[..., None]
@@ -506,7 +509,7 @@ def _exact_decode(s):
     for i, length in enumerate(s["lens"].tolist()):
         ids = s["table"][i, : -(-length // B)]
         for h in range(H):
-            K, V = (_exact_rows(s[p], ids, h, length, B, D) for p in ("k_pool", "v_pool"))
+            K, V = (_exact_rows(s, x, ids, h, length, B, D) for x in "kv")
             w = torch.softmax(s["q"][i, h * G : (h + 1) * G].double() @ K.T * D**-0.5, -1)
             out[i, h * G : (h + 1) * G] = w @ V
     return out
@@ -522,7 +525,7 @@ def _exact_prefill(s):
         ids = s["table"][i, : -(-(past + n) // B)]
         seen = torch.ones(n, past + n, dtype=torch.bool, device=DEV).tril(past)
         for h in range(H):
-            K, V = (_exact_rows(s[p], ids, h, past + n, B, D) for p in ("k_pool", "v_pool"))
+            K, V = (_exact_rows(s, x, ids, h, past + n, B, D) for x in "kv")
             for e in range(h * G, (h + 1) * G):
                 x = s["q"][at : at + n, e].double() @ K.T * D**-0.5
                 out[at : at + n, e] = torch.softmax(torch.where(seen, x, float("-inf")), -1) @ V
