@@ -74,7 +74,23 @@ enum {
  * (float32 division, ties to even) clamped to [-127, 127], an all-zero group
  * having d = 0 and zero codes.  q, new K/V rows and outputs as for FP8.
  * D_h a multiple of 32; device work needs the scale arrays. */
-enum { KV_DTYPE_F32 = 0, KV_DTYPE_BF16 = 1, KV_DTYPE_FP8_E4M3 = 2, KV_DTYPE_Q8_0 = 3 };
+enum { KV_DTYPE_F32 = 0, KV_DTYPE_BF16 = 1, KV_DTYPE_FP8_E4M3 = 2, KV_DTYPE_Q8_0 = 3,
+       KV_DTYPE_Q4_0 = 4 };
+/* KV_DTYPE_Q4_0: the pages' q4_0 ([IO] §8.4.2, Fig. 8-23): every group of 32
+ * consecutive values of a (slot, head) row shares one fp16 scale d and keeps a
+ * 4-bit code c in [-7, 7] each, x ~ c * d (18 bytes per 32 values, against 64
+ * for BF16).  A written group's scale is the fp16 nearest to max |x| / 7
+ * (float32 division), each code the integer nearest to x / d (float32
+ * division, ties to even) clamped to [-7, 7], an all-zero group having d = 0
+ * and zero codes.  Scales and codes share the caches, one chunk of
+ * B * (D_h / 2 + D_h / 16) bytes per (layer, block, K/V head):
+ *   K_cache, V_cache : bytes [N_layers][N_blocks][H_kv][chunk]
+ *   chunk            : codes [D_h / 32][B][16], then fp16 scales, of K
+ *                      [B][D_h / 32] and of V [D_h / 32][B]
+ * byte i of a group's 16 holds value 2i in its low nibble and 2i + 1 in its
+ * high one, code c as c + 8.  A (block, head) is one contiguous copy, and a
+ * group's rows are adjacent 16-byte vectors.  q, new K/V rows and outputs as
+ * for FP8. */
 
 /* bits of the device status word */
 enum {
@@ -103,11 +119,14 @@ const char* kv_status_string(kvStatus s);
  * Supported: block_size 1..256, head_dim 64 or 128, dtype F32 or BF16;
  * FP8_E4M3 with head_dim 128 and block_size a multiple of 8 that divides 64
  * or is a multiple of it (decode on either tensor-core pass); Q8_0 with
- * FP8's shapes (decode on the warp-level pass).  Creation itself fails with
- * KV_ERR_INVALID_ARG only for non-positive sizes, block_size > 256, an
- * unknown dtype, or (Q8_0) a head_dim not a multiple of 32 or H_kv *
- * block_size * head_dim / 16 scale bytes per block not a multiple of 16;
- * device calls on other unsupported shapes return KV_ERR_UNSUPPORTED. */
+ * FP8's shapes (decode on the warp-level pass); Q4_0 with FP8's block sizes
+ * and head_dim 64 or 128 (decode on its own warp-level pass).  Creation itself
+ * fails with KV_ERR_INVALID_ARG only for non-positive sizes, block_size > 256,
+ * an unknown dtype, (Q8_0) a head_dim not a multiple of 32 or H_kv *
+ * block_size * head_dim / 16 scale bytes per block not a multiple of 16, or
+ * (Q4_0) a head_dim not a multiple of 32 or block_size * head_dim / 16 scale
+ * bytes per chunk not a multiple of 16; device calls on other unsupported
+ * shapes return KV_ERR_UNSUPPORTED. */
 kvStatus kv_pool_create(int n_layers, int n_blocks, int block_size, int n_kv_heads,
                         int head_dim, int dtype, void* k_cache, void* v_cache,
                         int32_t* d_status, const int32_t* free_order, kvPool** out);
@@ -128,8 +147,8 @@ kvStatus kv_block_refcount(const kvPool* pool, int32_t id, int* out);
 
 /* Pool options.  KV_OPT_DECODE_PATH selects the split-pass kernel:
  * 0 = automatic (warp-level tensor-core pass for bfloat16 pools whose block
- * size is a multiple of 8 and for FP8 and q8_0 pools, CUDA-core pass
- * otherwise), 1 = always the CUDA-core pass (not for FP8 or q8_0 pools), 2 =
+ * size is a multiple of 8 and for FP8, q8_0 and q4_0 pools, CUDA-core pass
+ * otherwise), 1 = always the CUDA-core pass (not for FP8, q8_0 or q4_0 pools), 2 =
  * the warp-level tensor-core pass (mma.sync) where the pool allows it, 3 =
  * the tcgen05 pass (tensor-memory accumulators; bfloat16 or FP8, D_h = 128)
  * where the pool allows it, else as 2.  A plan (paged_decode_plan)
@@ -145,8 +164,13 @@ kvStatus kv_block_refcount(const kvPool* pool, int32_t id, int* out);
  * per-CTA start records (value in 1 .. 1024; 0, the default = the split
  * pass's own count once the device is known).  Records built for another
  * count than the launch's are ignored (the kernel then searches the plan);
- * results are the same either way. */
-enum { KV_OPT_DECODE_PATH = 1, KV_OPT_PDL = 2, KV_OPT_PLAN_GRID = 3 };
+ * results are the same either way.  KV_OPT_DEVICE_TABLES: 0 (default) = block
+ * tables, context lengths and chunk starts were written by the host before the
+ * stream's kernels that read them were launched (attention kernels read them
+ * while their predecessor finishes); 1 = kernels or copies earlier in the
+ * stream may write them, and attention reads them only after its predecessors.
+ * paged_tables_append and paged_tables_release set it on their pool. */
+enum { KV_OPT_DECODE_PATH = 1, KV_OPT_PDL = 2, KV_OPT_PLAN_GRID = 3, KV_OPT_DEVICE_TABLES = 4 };
 kvStatus kv_pool_set_option(kvPool* pool, int option, int value);
 
 /* Scales of an FP8_E4M3 pool (default 1, 1): a written value x is stored as
@@ -282,6 +306,16 @@ kvStatus cow_copy(kvPool* pool, const int32_t* d_pairs, int n_pairs, void* strea
  * with k_new / v_new laid out [N_layers][n_tokens][H_kv][D_h]. */
 kvStatus reshape_and_cache(kvPool* pool, int layer, const void* d_k_new, const void* d_v_new,
                            const int64_t* d_slot_mapping, int n_tokens, void* stream);
+
+/* Read rows back, the inverse of reshape_and_cache: token i's K and V rows
+ * [H_kv][D_h] of `layer` at slot d_slots[i], as float32 or bfloat16
+ * (out_dtype): the stored elements, or a quantized pool's codes times their
+ * scale (float32 product; bfloat16 rounds it to nearest even).  A negative
+ * slot leaves the token's output rows as they were.  layer == -1 reads every
+ * layer, outputs laid out [N_layers][n_tokens][H_kv][D_h].  Any pool dtype;
+ * outputs 16-byte aligned. */
+kvStatus gather_cached_rows(kvPool* pool, int layer, const int64_t* d_slots, int n_tokens,
+                            void* d_k_out, void* d_v_out, int out_dtype, void* stream);
 
 /* Bytes of decode workspace for n_seq sequences with n_q_heads query heads.
  * Independent of the context lengths. */

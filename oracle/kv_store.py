@@ -20,7 +20,8 @@ patterns, and a gather returns ``code value * scale``.  ``"q8_0"`` pools
 hold int8 codes (uint8 bits) of the written values and one fp16 scale per
 group of 32 values of a (slot, head) row, ``Ks`` / ``Vs [N_layers,
 N_blocks, B, H_kv, D_h / 32]`` (uint16 bits; ``oracle.q8``); a gather
-returns ``code * scale``.
+returns ``code * scale``.  ``"q4_0"`` pools hold packed 4-bit codes, two a
+byte, ``[..., D_h / 2]``, and scales like q8_0's (``oracle.q4``).
 """
 
 from __future__ import annotations
@@ -28,11 +29,16 @@ from __future__ import annotations
 import numpy as np
 
 from .fp8 import e4m3_decode, e4m3_encode
+from .q4 import q4_decode, q4_encode
 from .q8 import GROUP, q8_decode, q8_encode
 
-STORAGE = {"f32": np.float32, "bf16": np.uint16, "fp8_e4m3": np.uint8, "q8_0": np.uint8}
+STORAGE = {"f32": np.float32, "bf16": np.uint16, "fp8_e4m3": np.uint8, "q8_0": np.uint8,
+           "q4_0": np.uint8}
 # dtype of the rows a caller writes (and of q) for each pool dtype
-INPUT_DTYPE = {"f32": "f32", "bf16": "bf16", "fp8_e4m3": "bf16", "q8_0": "bf16"}
+INPUT_DTYPE = {"f32": "f32", "bf16": "bf16", "fp8_e4m3": "bf16", "q8_0": "bf16",
+               "q4_0": "bf16"}
+# (encode, decode) of the formats with a scale per 32 values
+GROUP_CODES = {"q8_0": (q8_encode, q8_decode), "q4_0": (q4_encode, q4_decode)}
 
 
 def to_f64(x: np.ndarray, dtype: str) -> np.ndarray:
@@ -52,19 +58,22 @@ class KVStore:
         self.H, self.D, self.dtype = n_kv_heads, head_dim, dtype
         self.k_scale, self.v_scale = float(k_scale), float(v_scale)
         shape = (n_layers, n_blocks, block_size, n_kv_heads, head_dim)
+        if dtype == "q4_0":
+            shape = shape[:-1] + (head_dim // 2,)
         self.K = np.zeros(shape, dtype=STORAGE[dtype])
         self.V = np.zeros(shape, dtype=STORAGE[dtype])
-        if dtype == "q8_0":
+        if dtype in GROUP_CODES:
             sshape = shape[:-1] + (head_dim // GROUP,)
             self.Ks = np.zeros(sshape, dtype=np.uint16)
             self.Vs = np.zeros(sshape, dtype=np.uint16)
 
     def write_slot(self, layer: int, slot: int, k_row, v_row) -> None:
         p, o = divmod(int(slot), self.B)
-        if self.dtype == "q8_0":
+        if self.dtype in GROUP_CODES:
             # rows arrive as bf16 patterns; each head's row in groups of 32
-            kc, ks = q8_encode(to_f64(k_row, "bf16").astype(np.float32))
-            vc, vs = q8_encode(to_f64(v_row, "bf16").astype(np.float32))
+            encode = GROUP_CODES[self.dtype][0]
+            kc, ks = encode(to_f64(k_row, "bf16").astype(np.float32))
+            vc, vs = encode(to_f64(v_row, "bf16").astype(np.float32))
             self.K[layer, p, o], self.Ks[layer, p, o] = kc, ks
             self.V[layer, p, o], self.Vs[layer, p, o] = vc, vs
             return
@@ -89,7 +98,7 @@ class KVStore:
         K and V, into block ``dst``."""
         self.K[:, dst] = self.K[:, src]
         self.V[:, dst] = self.V[:, src]
-        if self.dtype == "q8_0":
+        if self.dtype in GROUP_CODES:
             self.Ks[:, dst] = self.Ks[:, src]
             self.Vs[:, dst] = self.Vs[:, src]
 
@@ -105,7 +114,7 @@ class KVStore:
             rows = min(self.B, ctx - j * self.B)
             ks.append(self.K[layer, p, :rows])
             vs.append(self.V[layer, p, :rows])
-        shape = (0, self.H, self.D)
+        shape = (0, self.H, self.K.shape[-1])
         k = np.concatenate(ks) if ks else np.zeros(shape, dtype=self.K.dtype)
         v = np.concatenate(vs) if vs else np.zeros(shape, dtype=self.V.dtype)
         return k, v
@@ -116,7 +125,8 @@ class KVStore:
         k, v = self.gather_raw(layer, table, ctx)
         if self.dtype == "fp8_e4m3":
             return e4m3_decode(k) * self.k_scale, e4m3_decode(v) * self.v_scale
-        if self.dtype == "q8_0":
+        if self.dtype in GROUP_CODES:
+            decode = GROUP_CODES[self.dtype][1]
             ks, vs = [], []
             for j in range(-(-ctx // self.B)):
                 rows = min(self.B, ctx - j * self.B)
@@ -125,5 +135,5 @@ class KVStore:
             shape = (0, self.H, self.D // GROUP)
             sk = np.concatenate(ks) if ks else np.zeros(shape, dtype=np.uint16)
             sv = np.concatenate(vs) if vs else np.zeros(shape, dtype=np.uint16)
-            return q8_decode(k, sk), q8_decode(v, sv)
+            return decode(k, sk), decode(v, sv)
         return to_f64(k, self.dtype), to_f64(v, self.dtype)

@@ -31,10 +31,12 @@ KV_ERR_SCRATCH_TOO_SMALL = 7
 KV_OPT_DECODE_PATH = 1
 KV_OPT_PDL = 2
 KV_OPT_PLAN_GRID = 3
+KV_OPT_DEVICE_TABLES = 4
 KV_DTYPE_F32 = 0
 KV_DTYPE_BF16 = 1
 KV_DTYPE_FP8_E4M3 = 2
 KV_DTYPE_Q8_0 = 3
+KV_DTYPE_Q4_0 = 4
 # bits of the device status word
 KV_DEV_BAD_BLOCK_ID = 1
 KV_DEV_BAD_SLOT = 2
@@ -88,6 +90,7 @@ SIGNATURES = [
     ("seq_block_table", C.c_int, [_vp, _i32p, C.c_int, C.c_int, _i32p, _i32p]),
     ("cow_copy", C.c_int, [_vp, _vp, C.c_int, _vp]),
     ("reshape_and_cache", C.c_int, [_vp, C.c_int, _vp, _vp, _vp, C.c_int, _vp]),
+    ("gather_cached_rows", C.c_int, [_vp, C.c_int, _vp, C.c_int, _vp, _vp, C.c_int, _vp]),
     ("paged_decode_workspace_bytes", C.c_size_t, [_vp, C.c_int, C.c_int]),
     ("paged_decode_partials", C.c_int, [_vp, C.c_int, _vp, C.c_int, _vp, C.c_int, _vp, C.c_int,
                                         C.c_float, _vp, C.c_size_t, _vp]),

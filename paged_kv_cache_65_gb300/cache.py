@@ -1,8 +1,9 @@
 """Python face of the C ABI: one object per pool.
 
 ``PagedKVCache`` owns the device tensors (allocated with torch: K and V pools
-``[N_layers, N_blocks, B, H_kv, D_h]`` and a status word) and the library's
-pool handle.  Each method forwards to the C function of the same name;
+``[N_layers, N_blocks, B, H_kv, D_h]``, for a q4_0 pool the chunks ``[N_layers,
+N_blocks, H_kv, B * D_h * 9 / 16]`` of bytes, and a status word) and the
+library's pool handle.  Each method forwards to the C function of the same name;
 nothing here computes any part of the method.
 """
 
@@ -16,7 +17,7 @@ from . import _lib
 from ._lib import check, i32, lib, ptr_f32, ptr_i32, ptr_i64, vp
 
 DTYPES = {"f32": _lib.KV_DTYPE_F32, "bf16": _lib.KV_DTYPE_BF16, "fp8_e4m3": _lib.KV_DTYPE_FP8_E4M3,
-          "q8_0": _lib.KV_DTYPE_Q8_0}
+          "q8_0": _lib.KV_DTYPE_Q8_0, "q4_0": _lib.KV_DTYPE_Q4_0}
 
 
 def _stream(stream) -> C.c_void_p:
@@ -47,8 +48,10 @@ class PagedKVCache:
             import torch
 
             tdt = {"f32": torch.float32, "bf16": torch.bfloat16, "fp8_e4m3": torch.uint8,
-                   "q8_0": torch.uint8}[dtype]
+                   "q8_0": torch.uint8, "q4_0": torch.uint8}[dtype]
             shape = (n_layers, n_blocks, block_size, n_kv_heads, head_dim)
+            if dtype == "q4_0":  # codes and scales of a (block, head) side by side
+                shape = (n_layers, n_blocks, n_kv_heads, block_size * head_dim * 9 // 16)
             self.k = torch.empty(shape, dtype=tdt, device=device)
             self.v = torch.empty(shape, dtype=tdt, device=device)
             if dtype == "q8_0":
@@ -220,6 +223,15 @@ class PagedKVCache:
     def reshape_and_cache(self, layer, k_new, v_new, d_slots, n_tokens, stream=None):
         check(lib.reshape_and_cache(self.handle, int(layer), vp(k_new), vp(v_new), vp(d_slots),
                                     int(n_tokens), _stream(stream)), "reshape_and_cache")
+
+    def gather_cached_rows(self, layer, d_slots, n_tokens, k_out, v_out, stream=None):
+        """The K and V rows at the listed slots, as ``k_out``'s dtype (float32
+        or bfloat16); tokens with a negative slot keep their output rows."""
+        if k_out.dtype != v_out.dtype:
+            raise TypeError("k_out and v_out have one dtype")
+        check(lib.gather_cached_rows(self.handle, int(layer), vp(d_slots), int(n_tokens),
+                                     vp(k_out), vp(v_out), _out_dtype(k_out), _stream(stream)),
+              "gather_cached_rows")
 
     def paged_decode_workspace_bytes(self, n_seq, n_q_heads):
         return int(lib.paged_decode_workspace_bytes(self.handle, int(n_seq), int(n_q_heads)))

@@ -241,13 +241,18 @@ kvStatus kv_pool_create(int n_layers, int n_blocks, int block_size, int n_kv_hea
   if (n_layers <= 0 || n_blocks <= 0 || block_size <= 0 || block_size > 256 || n_kv_heads <= 0 ||
       head_dim <= 0 ||
       (dtype != KV_DTYPE_F32 && dtype != KV_DTYPE_BF16 && dtype != KV_DTYPE_FP8_E4M3 &&
-       dtype != KV_DTYPE_Q8_0))
+       dtype != KV_DTYPE_Q8_0 && dtype != KV_DTYPE_Q4_0))
     return KV_ERR_INVALID_ARG;
   // q8_0: whole groups of 32 per head row, and one block's scales of a head
   // (B * D_h / 32 fp16) times H_kv in whole 16-byte vectors
   if (dtype == KV_DTYPE_Q8_0 &&
       (head_dim % 32 != 0 ||
        (static_cast<int64_t>(n_kv_heads) * block_size * (head_dim / 32) * 2) % 16 != 0))
+    return KV_ERR_INVALID_ARG;
+  // q4_0: whole groups of 32 per head row, and a chunk's scales (B * D_h / 32
+  // fp16) in whole 16-byte vectors, so that every chunk starts on one
+  if (dtype == KV_DTYPE_Q4_0 &&
+      (head_dim % 32 != 0 || (static_cast<int64_t>(block_size) * (head_dim / 32) * 2) % 16 != 0))
     return KV_ERR_INVALID_ARG;
   if ((k_cache == nullptr) != (v_cache == nullptr)) return KV_ERR_INVALID_ARG;
   const int esize = dtype == KV_DTYPE_F32 ? 4 : (dtype == KV_DTYPE_BF16 ? 2 : 1);
@@ -360,6 +365,10 @@ kvStatus kv_pool_set_option(kvPool* p, int option, int value) {
   }
   if (option == KV_OPT_PDL && (value == 0 || value == 1)) {
     p->pdl = value == 1;
+    return KV_OK;
+  }
+  if (option == KV_OPT_DEVICE_TABLES && (value == 0 || value == 1)) {
+    p->device_tables = value == 1;
     return KV_OK;
   }
   if (option == KV_OPT_PLAN_GRID && value >= 0 && value <= kMaxDecodeCtas) {

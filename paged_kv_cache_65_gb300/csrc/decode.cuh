@@ -72,7 +72,8 @@ struct DecodeArgs {
   // rows [plan row][H_kv][D_h] of this layer (bfloat16) of each listed
   // sequence's newest token, its last context position, written into the
   // pool (k_pool / v_pool, FP8 pools as codes of x / k_scale_w, v_scale_w)
-  // by the CTA that reads the block holding it, before that read
+  // by the CTA that reads the block holding it, before that read.  The q4_0
+  // pass reads the pool through k_pool / v_pool
   const void* k_new = nullptr;
   const void* v_new = nullptr;
   void* k_pool = nullptr;
@@ -81,6 +82,8 @@ struct DecodeArgs {
   // q8_0 pools: the fp16 scales [L][N][H_kv][B][D / 32] of K and V
   const void* k_sc = nullptr;
   const void* v_sc = nullptr;
+  // q4_0 pass: tables and lengths are read only after the previous grid
+  bool meta_wait = false;
 };
 
 constexpr int ilog2(int x) { return x <= 1 ? 0 : 1 + ilog2(x / 2); }

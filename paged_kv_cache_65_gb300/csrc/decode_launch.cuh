@@ -94,6 +94,11 @@ cudaError_t launch_mma_q8(int D, int G, const CUtensorMap& tk, const CUtensorMap
                           const DecodeArgs& a, int sm_count, int max_grid, int* grid_io,
                           cudaStream_t st, bool pdl, bool* supported);
 
+// The pass over a q4_0 pool (4-bit codes, fp16 scales per 32 values, read
+// through a.k_pool / a.v_pool), D_h 64 or 128.
+cudaError_t launch_decode_q4(int D, const DecodeArgs& a, int sm_count, int max_grid, int* grid_io,
+                             cudaStream_t st, bool pdl, bool* supported);
+
 // Dispatch over (D, G) for one element size; *supported = false when the
 // shape has no compiled instantiation.
 cudaError_t launch_split_e2(int D, int G, const CUtensorMap& tk, const CUtensorMap& tv,

@@ -12,6 +12,7 @@
 #include "decode_launch.cuh"
 #include "prefill.h"
 #include "launch.cuh"
+#include "rows.h"
 #include "plan.h"
 #include "pool.h"
 #include "ptx.cuh"
@@ -96,7 +97,10 @@ kvStatus ensure_device(kvPool* p) {
     return KV_ERR_CUDA;
   if (p->dtype == KV_DTYPE_Q8_0 && (!p->k_sc || !p->v_sc))
     return KV_ERR_INVALID_ARG;  // a q8_0 pool needs its scale arrays
-  if (pool_codes8(p)) {
+  if (p->dtype == KV_DTYPE_Q4_0) {  // read by untiled bulk copies: no descriptors
+    if (!pool_tensor_core_shape(p)) return KV_ERR_UNSUPPORTED;
+    p->mma_ok = true;
+  } else if (pool_codes8(p)) {
     // FP8 / q8_0 codes: the tensor-core passes (q8_0: the warp-level one),
     // one 128-byte swizzled box (128 codes, all of D_h = 128) by
     // mma_box_rows(B, 128) rows
@@ -692,7 +696,8 @@ kvStatus prefill_common(kvPool* p, int layer, const void* d_q, int n_q_heads,
   const CUtensorMap& tk = stage ? *stage->tk : *reinterpret_cast<const CUtensorMap*>(p->tmap[2]);
   const CUtensorMap& tv = stage ? *stage->tv : *reinterpret_cast<const CUtensorMap*>(p->tmap[3]);
   const cudaError_t e =
-      pkv::launch_prefill_tc(tk, tv, a, max_chunk, n_items, as_stream(stream), p->pdl);
+      pkv::launch_prefill_tc(tk, tv, a, max_chunk, n_items, as_stream(stream),
+                             p->pdl && !p->device_tables);
   return e == cudaSuccess ? KV_OK : KV_ERR_CUDA;
 }
 
@@ -764,7 +769,7 @@ kvStatus cow_copy(kvPool* p, const int32_t* d_pairs, int n_pairs, void* stream) 
   if (n_pairs == 0) return KV_OK;
   kvStatus s = ensure_device(p);
   if (s != KV_OK) return s;
-  const long long block_vecs = static_cast<long long>(p->B) * p->H * p->D * p->esize / 16;
+  const long long block_vecs = pool_block_bytes(p) / 16;
   // about 512 vectors of K (and of V) per CTA: two per thread
   const long long want = (block_vecs + 511) / 512;
   const int parts = static_cast<int>(want < 1 ? 1 : (want > 16 ? 16 : want));
@@ -791,6 +796,12 @@ kvStatus reshape_and_cache(kvPool* p, int layer, const void* d_k_new, const void
   if (!aligned16(d_k_new) || !aligned16(d_v_new)) return KV_ERR_INVALID_ARG;
   kvStatus s = ensure_device(p);
   if (s != KV_OK) return s;
+  if (p->dtype == KV_DTYPE_Q4_0) {
+    const cudaError_t e =
+        pkv::launch_slot_write_q4(p, layer, d_k_new, d_v_new, d_slot_mapping, n_tokens,
+                                  as_stream(stream));
+    return e == cudaSuccess ? KV_OK : KV_ERR_CUDA;
+  }
   if (p->dtype == KV_DTYPE_Q8_0) {
     const int groups = p->H * p->D / 32;
     dim3 grid(n_tokens, layer >= 0 ? 1 : p->L);
@@ -823,6 +834,20 @@ kvStatus reshape_and_cache(kvPool* p, int layer, const void* d_k_new, const void
       reinterpret_cast<const uint4*>(d_k_new), reinterpret_cast<const uint4*>(d_v_new),
       d_slot_mapping, n_tokens, reinterpret_cast<uint4*>(p->k), reinterpret_cast<uint4*>(p->v),
       layer, static_cast<long long>(p->N) * p->B, row_vecs, p->d_status);
+  return e == cudaSuccess ? KV_OK : KV_ERR_CUDA;
+}
+
+kvStatus gather_cached_rows(kvPool* p, int layer, const int64_t* d_slots, int n_tokens,
+                            void* d_k_out, void* d_v_out, int out_dtype, void* stream) {
+  if (!p || n_tokens < 0 || layer < -1 || layer >= p->L) return KV_ERR_INVALID_ARG;
+  if (out_dtype != KV_DTYPE_F32 && out_dtype != KV_DTYPE_BF16) return KV_ERR_INVALID_ARG;
+  if (n_tokens == 0) return KV_OK;
+  if (!d_slots || !d_k_out || !d_v_out || !aligned16(d_k_out) || !aligned16(d_v_out))
+    return KV_ERR_INVALID_ARG;
+  kvStatus s = ensure_device(p);
+  if (s != KV_OK) return s;
+  const cudaError_t e = pkv::launch_gather_rows(p, layer, d_slots, n_tokens, d_k_out, d_v_out,
+                                                out_dtype, as_stream(stream));
   return e == cudaSuccess ? KV_OK : KV_ERR_CUDA;
 }
 
@@ -873,15 +898,25 @@ kvStatus paged_decode_partials(kvPool* p, int layer, const void* d_q, int n_q_he
   a.plan_W = 0;
   a.starts = nullptr;
   a.start_grid = 0;
+  a.k_pool = p->k;
+  a.v_pool = p->v;
+  a.meta_wait = p->device_tables;
   const DecodeKernel kern = decode_kernel(p);
+  // kernels other than the q4_0 pass read tables and lengths before waiting
+  // for the previous grid: launched after it when the device writes those
+  const bool pdl = p->pdl && !p->device_tables;
   int* grid_io = kern == kKernelTc ? &p->grid_tc : &p->grid_by_g[ilog2_small(G)];
   bool supported = false;
   cudaError_t e;
-  if (p->dtype == KV_DTYPE_FP8_E4M3 && kern == kKernelTc) {
+  if (p->dtype == KV_DTYPE_Q4_0) {
+    if (kern != kKernelMma) return KV_ERR_UNSUPPORTED;  // no CUDA-core pass over codes
+    e = pkv::launch_decode_q4(p->D, a, p->sm_count, kMaxDecodeCtas, grid_io, as_stream(stream),
+                              p->pdl, &supported);
+  } else if (p->dtype == KV_DTYPE_FP8_E4M3 && kern == kKernelTc) {
     const CUtensorMap& tk = *reinterpret_cast<const CUtensorMap*>(p->tmap[2]);
     const CUtensorMap& tv = *reinterpret_cast<const CUtensorMap*>(p->tmap[3]);
     e = pkv::launch_tc_fp8(tk, tv, a, p->sm_count, kMaxDecodeCtas, grid_io, as_stream(stream),
-                           p->pdl);
+                           pdl);
     supported = true;
   } else if (pool_codes8(p)) {
     if (kern != kKernelMma) return KV_ERR_UNSUPPORTED;  // no CUDA-core pass over codes
@@ -891,27 +926,27 @@ kvStatus paged_decode_partials(kvPool* p, int layer, const void* d_q, int n_q_he
     a.v_sc = p->v_sc;
     e = p->dtype == KV_DTYPE_Q8_0
             ? pkv::launch_mma_q8(p->D, G, tk, tv, a, p->sm_count, kMaxDecodeCtas, grid_io,
-                                 as_stream(stream), p->pdl, &supported)
+                                 as_stream(stream), pdl, &supported)
             : pkv::launch_mma_fp8(p->D, G, tk, tv, a, p->sm_count, kMaxDecodeCtas, grid_io,
-                                  as_stream(stream), p->pdl, &supported);
+                                  as_stream(stream), pdl, &supported);
   } else if (kern == kKernelTc) {
     const CUtensorMap& tk = *reinterpret_cast<const CUtensorMap*>(p->tmap[2]);
     const CUtensorMap& tv = *reinterpret_cast<const CUtensorMap*>(p->tmap[3]);
     e = pkv::launch_tc_bf16(tk, tv, a, p->sm_count, kMaxDecodeCtas, grid_io, as_stream(stream),
-                            p->pdl);
+                            pdl);
     supported = true;
   } else if (kern == kKernelMma) {
     const CUtensorMap& tk = *reinterpret_cast<const CUtensorMap*>(p->tmap[2]);
     const CUtensorMap& tv = *reinterpret_cast<const CUtensorMap*>(p->tmap[3]);
     e = pkv::launch_mma_bf16(p->D, G, tk, tv, a, p->sm_count, kMaxDecodeCtas, grid_io,
-                             as_stream(stream), p->pdl, &supported);
+                             as_stream(stream), pdl, &supported);
   } else {
     const CUtensorMap& tk = *reinterpret_cast<const CUtensorMap*>(p->tmap[0]);
     const CUtensorMap& tv = *reinterpret_cast<const CUtensorMap*>(p->tmap[1]);
     e = p->esize == 2 ? pkv::launch_split_e2(p->D, G, tk, tv, a, p->sm_count, kMaxDecodeCtas,
-                                             grid_io, as_stream(stream), p->pdl, &supported)
+                                             grid_io, as_stream(stream), pdl, &supported)
                       : pkv::launch_split_e4(p->D, G, tk, tv, a, p->sm_count, kMaxDecodeCtas,
-                                             grid_io, as_stream(stream), p->pdl, &supported);
+                                             grid_io, as_stream(stream), pdl, &supported);
   }
   if (!supported) return KV_ERR_UNSUPPORTED;
   return e == cudaSuccess ? KV_OK : KV_ERR_CUDA;
@@ -1049,25 +1084,31 @@ kvStatus partials_planned(kvPool* p, int layer, const void* d_q, int n_q_heads,
   a.v_scale_w = p->v_scale;
   a.k_sc = p->k_sc;
   a.v_sc = p->v_sc;
+  a.meta_wait = p->device_tables;
+  const bool pdl = p->pdl && !p->device_tables;  // as in paged_decode_partials
   const CUtensorMap& tk = *reinterpret_cast<const CUtensorMap*>(p->tmap[2]);
   const CUtensorMap& tv = *reinterpret_cast<const CUtensorMap*>(p->tmap[3]);
   bool supported = true;
   const cudaError_t e =
       tc ? (p->dtype == KV_DTYPE_FP8_E4M3
                 ? pkv::launch_tc_fp8(tk, tv, a, p->sm_count, kMaxDecodeCtas, &p->grid_tc,
-                                     as_stream(stream), p->pdl)
+                                     as_stream(stream), pdl)
                 : pkv::launch_tc_bf16(tk, tv, a, p->sm_count, kMaxDecodeCtas, &p->grid_tc,
-                                      as_stream(stream), p->pdl))
+                                      as_stream(stream), pdl))
+      : p->dtype == KV_DTYPE_Q4_0
+          ? pkv::launch_decode_q4(p->D, a, p->sm_count, kMaxDecodeCtas,
+                                  &p->grid_by_g[ilog2_small(G)], as_stream(stream), p->pdl,
+                                  &supported)
       : p->dtype == KV_DTYPE_Q8_0
           ? pkv::launch_mma_q8(p->D, G, tk, tv, a, p->sm_count, kMaxDecodeCtas,
-                               &p->grid_by_g[ilog2_small(G)], as_stream(stream), p->pdl,
+                               &p->grid_by_g[ilog2_small(G)], as_stream(stream), pdl,
                                &supported)
       : p->dtype == KV_DTYPE_FP8_E4M3
           ? pkv::launch_mma_fp8(p->D, G, tk, tv, a, p->sm_count, kMaxDecodeCtas,
-                                &p->grid_by_g[ilog2_small(G)], as_stream(stream), p->pdl,
+                                &p->grid_by_g[ilog2_small(G)], as_stream(stream), pdl,
                                 &supported)
           : pkv::launch_mma_bf16(p->D, G, tk, tv, a, p->sm_count, kMaxDecodeCtas,
-                                 &p->grid_by_g[ilog2_small(G)], as_stream(stream), p->pdl,
+                                 &p->grid_by_g[ilog2_small(G)], as_stream(stream), pdl,
                                  &supported);
   if (!supported) return KV_ERR_UNSUPPORTED;
   return e == cudaSuccess ? KV_OK : KV_ERR_CUDA;

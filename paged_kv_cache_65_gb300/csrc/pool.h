@@ -75,6 +75,7 @@ struct kvPool {
   bool mma_ok = false;                      // swizzled descriptors valid (bf16, B % 8 == 0)
   int decode_path = 0;                      // KV_OPT_DECODE_PATH
   bool pdl = true;                          // programmatic dependent launch
+  bool device_tables = false;               // KV_OPT_DEVICE_TABLES
 
   // host staging of kv_decode_step_host: the step's metadata (slots, copy
   // pairs, tables, lengths, plan) in page-locked memory, laid out as in the
@@ -99,7 +100,22 @@ inline bool pool_codes8(const kvPool* p) {
   return p->dtype == KV_DTYPE_FP8_E4M3 || p->dtype == KV_DTYPE_Q8_0;
 }
 
+// Bytes of a token's K (or V) row of one head in a q4_0 chunk: 4-bit codes and
+// one fp16 scale per 32 values.
+inline int q4_row_bytes(int D) { return D / 2 + D / 16; }
+
+// Bytes of one block of K (or of V) of one layer, all heads.
+inline long long pool_block_bytes(const kvPool* p) {
+  if (p->dtype == KV_DTYPE_Q4_0) return static_cast<long long>(p->B) * p->H * q4_row_bytes(p->D);
+  return static_cast<long long>(p->B) * p->H * p->D * p->esize;
+}
+
 inline bool pool_tensor_core_shape(const kvPool* p) {
+  if (p->dtype == KV_DTYPE_Q4_0) {
+    // stages of 128 tokens as whole units of min(B, 128) tokens (64 at B = 192)
+    return (p->D == 64 || p->D == 128) && p->B % 8 == 0 &&
+           (p->B <= 64 ? 64 % p->B == 0 : p->B % 64 == 0);
+  }
   if (pool_codes8(p)) {
     // FP8 / q8_0: rows of 128 one-byte codes, one 128-byte swizzled box per row set
     if (p->D != 128 || p->B % 8 != 0) return false;

@@ -1,0 +1,221 @@
+// Row writes into a q4_0 pool and row reads from any pool.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "launch.cuh"
+#include "ptx.cuh"
+#include "rows.h"
+
+namespace pkv {
+
+namespace {
+
+// Slot write into a q4_0 pool: one CTA per (token, layer).  Four lanes share a
+// group of 32 bfloat16 values, eight each (one 16-byte load): the group's
+// largest |x| by two shuffles, d = the fp16 nearest to it over 7 (float32 IEEE
+// division), codes = the integers nearest to x / d (float32 IEEE division,
+// ties to even) clamped to [-7, 7], stored as c + 8, zero when d is 0.  A
+// lane's eight nibbles are one 32-bit word, a group's four words its 16 bytes
+// of the chunk's code plane.
+__global__ void __launch_bounds__(256)
+    slot_write_q4_kernel(const uint4* __restrict__ k_new, const uint4* __restrict__ v_new,
+                         const int64_t* __restrict__ slots, int n_tok, unsigned char* kc,
+                         unsigned char* vc, int layer, int n_blocks, int B, int H, int GR,
+                         int32_t* status) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int i = blockIdx.x;
+  const int ly = layer >= 0 ? layer : blockIdx.y;
+  const int64_t slot = slots[i];
+  if (slot < 0) return;
+  if (slot >= static_cast<int64_t>(n_blocks) * B) {
+    if (threadIdx.x == 0) record_status(status, KV_DEV_BAD_SLOT);
+    return;
+  }
+  const int row = H * GR * 4;  // lanes (8-value vectors) of a token row
+  const long long src = ((layer >= 0 ? 0LL : (long long)blockIdx.y * n_tok) + i) * row;
+  const int blk = static_cast<int>(slot / B);
+  const int o = static_cast<int>(slot - static_cast<int64_t>(blk) * B);
+  const long long chunk_bytes = static_cast<long long>(B) * GR * 18;
+  const long long blk0 = (static_cast<long long>(ly) * n_blocks + blk) * H;
+  // K lanes, then V lanes: both multiples of 4, so a group's lanes run together
+  for (int v = threadIdx.x; v < 2 * row; v += blockDim.x) {
+    const unsigned quad = 0xfu << (threadIdx.x & 28);
+    const bool is_k = v < row;
+    const int vv = is_k ? v : v - row;
+    const uint4 x = (is_k ? k_new : v_new)[src + vv];
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    float f[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      f[2 * k] = __uint_as_float(w[k] << 16);
+      f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+    }
+    float amax = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(f[k]));
+    amax = fmaxf(amax, __shfl_xor_sync(quad, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(quad, amax, 2));
+    const __half d16 = __float2half_rn(__fdiv_rn(amax, 7.f));
+    const float d = __half2float(d16);
+    uint32_t word = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      float c = d > 0.f ? rintf(__fdiv_rn(f[k], d)) : 0.f;
+      c = fminf(fmaxf(c, -7.f), 7.f);
+      word |= static_cast<uint32_t>(static_cast<int>(c) + 8) << (4 * k);
+    }
+    const int gi = vv >> 2;  // group of the token row
+    const int h = gi / GR, q = gi - h * GR;
+    unsigned char* chunk = (is_k ? kc : vc) + (blk0 + h) * chunk_bytes;
+    reinterpret_cast<uint32_t*>(chunk + (static_cast<long long>(q) * B + o) * 16)[vv & 3] = word;
+    if ((vv & 3) == 0) {
+      __half* sc = reinterpret_cast<__half*>(chunk + static_cast<long long>(GR) * B * 16);
+      sc[is_k ? o * GR + q : q * B + o] = d16;
+    }
+  }
+}
+
+// Four consecutive values of a row as float32.
+template <int DT>
+struct RowSource {
+  const unsigned char* cache;  // K or V
+  const unsigned char* scales; // q8_0
+  float scale;                 // FP8
+  int B, H, D, GR;
+  bool is_k;
+
+  // values 4 v .. 4 v + 3 of the row [H][D] at (block index incl. layer, offset)
+  __device__ __forceinline__ void load4(long long blk, int o, int v, float (&f)[4]) const {
+    const long long row = (blk * B + o) * H * D;
+    if constexpr (DT == KV_DTYPE_F32) {
+      const float4 x = reinterpret_cast<const float4*>(cache)[row / 4 + v];
+      f[0] = x.x;
+      f[1] = x.y;
+      f[2] = x.z;
+      f[3] = x.w;
+    } else if constexpr (DT == KV_DTYPE_BF16) {
+      const uint2 x = reinterpret_cast<const uint2*>(cache)[row / 4 + v];
+      f[0] = __uint_as_float(x.x << 16);
+      f[1] = __uint_as_float(x.x & 0xffff0000u);
+      f[2] = __uint_as_float(x.y << 16);
+      f[3] = __uint_as_float(x.y & 0xffff0000u);
+    } else if constexpr (DT == KV_DTYPE_FP8_E4M3) {
+      const uint32_t x = reinterpret_cast<const uint32_t*>(cache)[row / 4 + v];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        uint32_t h2;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(x >> (16 * k))));
+        f[2 * k] = scale * __half2float(__ushort_as_half(static_cast<unsigned short>(h2 & 0xffffu)));
+        f[2 * k + 1] = scale * __half2float(__ushort_as_half(static_cast<unsigned short>(h2 >> 16)));
+      }
+    } else if constexpr (DT == KV_DTYPE_Q8_0) {
+      const uint32_t x = reinterpret_cast<const uint32_t*>(cache)[row / 4 + v];
+      const int gi = v >> 3, h = gi / GR, q = gi - h * GR;
+      const float d = __half2float(
+          reinterpret_cast<const __half*>(scales)[((blk * H + h) * B + o) * GR + q]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        f[k] = d * static_cast<float>(static_cast<int8_t>((x >> (8 * k)) & 0xffu));
+    } else {
+      const int gi = v >> 3, h = gi / GR, q = gi - h * GR;
+      const unsigned char* chunk = cache + (blk * H + h) * (static_cast<long long>(B) * GR * 18);
+      const uint32_t x = reinterpret_cast<const uint16_t*>(
+          chunk + (static_cast<long long>(q) * B + o) * 16)[v & 7];
+      const float d = __half2float(reinterpret_cast<const __half*>(
+          chunk + static_cast<long long>(GR) * B * 16)[is_k ? o * GR + q : q * B + o]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        f[k] = d * static_cast<float>(static_cast<int>((x >> (4 * k)) & 15u) - 8);
+    }
+  }
+};
+
+// Rows at the listed slots: one CTA per (token, layer), four values a thread.
+template <int DT, bool BF16>
+__global__ void __launch_bounds__(256)
+    gather_rows_kernel(RowSource<DT> ks, RowSource<DT> vs, const int64_t* __restrict__ slots,
+                       int n_tok, int layer, int n_blocks, void* k_out, void* v_out,
+                       int32_t* status) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int i = blockIdx.x;
+  const int ly = layer >= 0 ? layer : blockIdx.y;
+  const int64_t slot = slots[i];
+  if (slot < 0) return;
+  if (slot >= static_cast<int64_t>(n_blocks) * ks.B) {
+    if (threadIdx.x == 0) record_status(status, KV_DEV_BAD_SLOT);
+    return;
+  }
+  const long long blk = static_cast<long long>(ly) * n_blocks + slot / ks.B;
+  const int o = static_cast<int>(slot % ks.B);
+  const int row = ks.H * ks.D / 4;
+  const long long dst = ((layer >= 0 ? 0LL : (long long)blockIdx.y * n_tok) + i) * row;
+  for (int v = threadIdx.x; v < 2 * row; v += blockDim.x) {
+    const bool is_k = v < row;
+    const int vv = is_k ? v : v - row;
+    float f[4];
+    (is_k ? ks : vs).load4(blk, o, vv, f);
+    void* out = is_k ? k_out : v_out;
+    if constexpr (BF16) {
+      const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]);
+      const __nv_bfloat162 b = __floats2bfloat162_rn(f[2], f[3]);
+      reinterpret_cast<uint2*>(out)[dst + vv] =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    } else {
+      reinterpret_cast<float4*>(out)[dst + vv] = make_float4(f[0], f[1], f[2], f[3]);
+    }
+  }
+}
+
+template <int DT>
+cudaError_t launch_gather(const kvPool* p, int layer, const int64_t* slots, int n_tokens,
+                          void* k_out, void* v_out, int out_dtype, cudaStream_t st) {
+  RowSource<DT> ks{static_cast<const unsigned char*>(p->k),
+                   static_cast<const unsigned char*>(p->k_sc), p->k_scale, p->B, p->H, p->D,
+                   p->D / 32, true};
+  RowSource<DT> vs{static_cast<const unsigned char*>(p->v),
+                   static_cast<const unsigned char*>(p->v_sc), p->v_scale, p->B, p->H, p->D,
+                   p->D / 32, false};
+  const int lanes = 2 * p->H * p->D / 4;
+  const int threads = lanes >= 256 ? 256 : (lanes + 31) / 32 * 32;
+  const dim3 grid(n_tokens, layer >= 0 ? 1 : p->L);
+  return launch_kernel(p->pdl,
+                       out_dtype == KV_DTYPE_BF16 ? gather_rows_kernel<DT, true>
+                                                  : gather_rows_kernel<DT, false>,
+                       grid, dim3(threads), 0, st, ks, vs, slots, n_tokens, layer, p->N, k_out,
+                       v_out, p->d_status);
+}
+
+}  // namespace
+
+cudaError_t launch_slot_write_q4(const kvPool* p, int layer, const void* k_new, const void* v_new,
+                                 const int64_t* slots, int n_tokens, cudaStream_t st) {
+  const int lanes = 2 * p->H * p->D / 8;
+  const int threads = lanes >= 256 ? 256 : (lanes + 31) / 32 * 32;
+  const dim3 grid(n_tokens, layer >= 0 ? 1 : p->L);
+  return launch_kernel(p->pdl, slot_write_q4_kernel, grid, dim3(threads), 0, st,
+                       static_cast<const uint4*>(k_new), static_cast<const uint4*>(v_new), slots,
+                       n_tokens, static_cast<unsigned char*>(p->k),
+                       static_cast<unsigned char*>(p->v), layer, p->N, p->B, p->H, p->D / 32,
+                       p->d_status);
+}
+
+cudaError_t launch_gather_rows(const kvPool* p, int layer, const int64_t* slots, int n_tokens,
+                               void* k_out, void* v_out, int out_dtype, cudaStream_t st) {
+  switch (p->dtype) {
+    case KV_DTYPE_F32:
+      return launch_gather<KV_DTYPE_F32>(p, layer, slots, n_tokens, k_out, v_out, out_dtype, st);
+    case KV_DTYPE_BF16:
+      return launch_gather<KV_DTYPE_BF16>(p, layer, slots, n_tokens, k_out, v_out, out_dtype, st);
+    case KV_DTYPE_FP8_E4M3:
+      return launch_gather<KV_DTYPE_FP8_E4M3>(p, layer, slots, n_tokens, k_out, v_out, out_dtype,
+                                              st);
+    case KV_DTYPE_Q8_0:
+      return launch_gather<KV_DTYPE_Q8_0>(p, layer, slots, n_tokens, k_out, v_out, out_dtype, st);
+    default:
+      return launch_gather<KV_DTYPE_Q4_0>(p, layer, slots, n_tokens, k_out, v_out, out_dtype, st);
+  }
+}
+
+}  // namespace pkv

@@ -91,7 +91,8 @@ def torch_seed(seed_words) -> int:
 
 def storage_dtype(dtype: str):
     """Element type of the values a caller writes (FP8 pools take bf16)."""
-    return {"f32": np.float32, "bf16": np.uint16, "fp8_e4m3": np.uint16, "q8_0": np.uint16}[dtype]
+    return {"f32": np.float32, "bf16": np.uint16, "fp8_e4m3": np.uint16, "q8_0": np.uint16,
+            "q4_0": np.uint16}[dtype]
 
 
 def storage_values(x: np.ndarray, dtype: str) -> np.ndarray:
@@ -100,7 +101,7 @@ def storage_values(x: np.ndarray, dtype: str) -> np.ndarray:
     x = np.ascontiguousarray(x, dtype=np.float32)
     if dtype == "f32":
         return x
-    if dtype in ("bf16", "fp8_e4m3", "q8_0"):  # code pools are written with bf16 rows
+    if dtype in ("bf16", "fp8_e4m3", "q8_0", "q4_0"):  # code pools are written with bf16 rows
         import torch
 
         t = torch.from_numpy(x).to(torch.bfloat16)
@@ -135,9 +136,10 @@ class Workload:
 
     @property
     def elem_bytes(self) -> float:
-        """Bytes of one stored K or V element (q8_0: its code and its share
-        of the group's 2-byte scale, 34 / 32)."""
-        return {"f32": 4, "bf16": 2, "fp8_e4m3": 1, "q8_0": 34 / 32}[self.dtype]
+        """Bytes of one stored K or V element (q8_0 and q4_0: its code and its
+        share of the group's 2-byte scale, 34 / 32 and 18 / 32)."""
+        return {"f32": 4, "bf16": 2, "fp8_e4m3": 1, "q8_0": 34 / 32,
+                "q4_0": 18 / 32}[self.dtype]
 
     # values --------------------------------------------------------------
     def append_values(self, value_seed: int, n_tokens: int):
