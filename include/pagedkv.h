@@ -100,7 +100,11 @@ enum {
   KV_DEV_WAIT_TIMEOUT = 8, /* a pipeline wait gave up (never expected;
                               kv_device_wait_selftest sets it on purpose) */
   KV_DEV_BAD_CONTEXT = 16, /* context_lens entry < 0 or > max_blocks * B */
-  KV_DEV_SMEM_ALIGN = 32   /* shared staging not 1 KiB aligned: pass skipped */
+  KV_DEV_SMEM_ALIGN = 32,  /* shared staging not 1 KiB aligned: pass skipped */
+  KV_DEV_NO_FREE_BLOCK = 64, /* device tables: the ring holds too few blocks;
+                                the batch was refused as a whole            */
+  KV_DEV_BAD_TABLE_ROW = 128 /* device tables: a bad row, count, length or
+                                ring state; the batch was refused as a whole */
 };
 
 typedef struct kvPool kvPool;
@@ -348,6 +352,79 @@ kvStatus paged_decode_attention(kvPool* pool, int layer, const void* d_q, int n_
                                 void* d_out, int out_dtype, void* d_workspace,
                                 size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------ device tables --
+ * Block tables and slot maps kept and built on the device, from the requests'
+ * token counts, so that a loop of steps needs no host reservation and no
+ * upload between them (a captured graph replays it).  The blocks come from
+ * the pool through block_alloc (the caller holds their handles) and wait in a
+ * FIFO ring of ids on the device; each row of the table set is one request's
+ * table, as seq_append_tokens would build it ([BT] §03-§05, §10): new blocks
+ * are taken from the ring's front in the batch's order when a token lands
+ * past the row's last block, and a released row's blocks go to its end.
+ * Blocks of a row are its own: no sharing and no copy-on-write. */
+typedef struct kvTables {
+  int32_t* tables;     /* device [n_rows][max_blocks], -1 past ceil(len / B)  */
+  int32_t* lens;       /* device [n_rows]: tokens of each row (0: not in use) */
+  int32_t* free_ids;   /* device [free_cap]: ring of free block ids           */
+  int64_t* free_state; /* device [2]: ring position of the oldest free id, and
+                          the number of free ids                              */
+  int n_rows;          /* up to 1,048,576 */
+  int max_blocks;
+  int free_cap;
+} kvTables;
+
+/* Append counts[i] tokens to row rows[i] for i = 0 .. n_seq - 1, as a whole or
+ * not at all.
+ *   d_rows   : [n_seq] rows, each listed once; -1 = an entry without a row (a
+ *              batch padded to a fixed size); null = rows 0 .. n_seq - 1
+ *   d_counts : [n_seq] new tokens, 0 or more; null = one each
+ *   max_tokens: length of d_slots and d_positions; more tokens than this in the
+ *              batch refuse it
+ * Outputs, each of which may be null:
+ *   d_slots       : int64 [max_tokens], the tokens' slots in batch order, -1
+ *                   past the last one (what reshape_and_cache takes)
+ *   d_positions   : int32 [max_tokens], their positions in their rows, -1 past
+ *   d_chunk_start : int32 [n_seq + 1], first token of each entry
+ *   d_block_table : int32 [n_seq][max_blocks], the listed rows' tables after
+ *                   the append, -1 padded (what the attention calls take)
+ *   d_context_lens: int32 [n_seq], their lengths after the append (0 for -1)
+ *   d_lens_out    : int32 [n_rows], every row's length after the append; null
+ *                   = written to t->lens
+ *   d_free_state_out: int64 [2], the ring's state after it; null = written to
+ *                   t->free_state
+ * New table entries are written to t->tables; outputs overlap no input and no
+ * other output, except d_lens_out and d_free_state_out the arrays they
+ * default to.  A batch
+ * that lists a row out of [-1, n_rows) or twice, has a negative count, a
+ * length outside [0, max_blocks * B], a row longer than that after it or more
+ * than max_tokens tokens sets KV_DEV_BAD_TABLE_ROW, one that needs more blocks
+ * than the ring holds KV_DEV_NO_FREE_BLOCK; both leave rows, lengths and ring
+ * as they were (copied to d_lens_out and d_free_state_out) and give the
+ * outputs of an empty batch (slots, positions and tables -1, starts and
+ * lengths 0).  A ring id outside the pool is flagged KV_DEV_BAD_BLOCK_ID and
+ * its tokens get slot -1.
+ *   d_workspace: paged_tables_workspace_bytes(pool, n_seq) bytes, 16-byte
+ *                aligned, not shared with a call in flight.
+ * Calls on one table set are ordered by the caller (one stream).  Sets the
+ * pool's KV_OPT_DEVICE_TABLES; other pools that attend through the tables need
+ * it set. */
+size_t paged_tables_workspace_bytes(const kvPool* pool, int n_seq);
+kvStatus paged_tables_append(kvPool* pool, const kvTables* t, const int32_t* d_rows,
+                             const int32_t* d_counts, int n_seq, int max_tokens, int64_t* d_slots,
+                             int32_t* d_positions, int32_t* d_chunk_start, int32_t* d_block_table,
+                             int32_t* d_context_lens, int32_t* d_lens_out,
+                             int64_t* d_free_state_out, void* d_workspace, size_t workspace_bytes,
+                             void* stream);
+
+/* Release the listed rows ([KC] release_sequence_blocks): their blocks go to
+ * the ring's end in the listed order, table order inside a row; entries become
+ * -1, lengths 0.  -1 entries are skipped.  A batch with a bad or repeated row,
+ * a bad length, or more blocks than the ring has room for sets
+ * KV_DEV_BAD_TABLE_ROW and changes nothing.  Workspace and ordering as
+ * paged_tables_append. */
+kvStatus paged_tables_release(kvPool* pool, const kvTables* t, const int32_t* d_rows, int n_seq,
+                              void* d_workspace, size_t workspace_bytes, void* stream);
+
 /* ------------------------------------------- sharing-aware decode plan --
  * Sequences that share physical blocks (after seq_fork, or a shared prompt;
  * [KC] zero-copy branching, [IO] §8.3.2) can have each shared block read
@@ -507,10 +584,13 @@ kvStatus paged_prefill_attention_scheduled(kvPool* pool, int layer, const void* 
  * copy with the K scale folded into the score scale and the outputs
  * multiplied by the V scale, so the results are those of attention over the
  * pool's dequantized values ([IO] §8.4.2: narrower KV read, wider
- * arithmetic).  Slots past a context are copied as zeros.
+ * arithmetic).  Slots past a context are copied as zeros.  A q4_0 pool (D_h =
+ * 128) is read through an fp16 copy the same way: the values c * d over a power
+ * of two per (sequence, K/V head), found by a kernel before, each rounded once
+ * to fp16's 11 bits, and the pass runs on fp16 operands.
  *   d_workspace : device buffer, 256-byte aligned, of at least
  *                 paged_prefill_staging_bytes(pool, n_seq, max_blocks)
- *                 bytes (0 for a bfloat16 pool); reused across calls, it
+ *                 bytes (0 for a pool read in place); reused across calls, it
  *                 must not be written while a call on it is in flight.
  * Errors as paged_prefill_attention; KV_ERR_UNSUPPORTED for other dtypes
  * or shapes; an out-of-range table entry is flagged KV_DEV_BAD_BLOCK_ID and

@@ -9,6 +9,6 @@ library has not been built.
 
 from . import _lib  # noqa: F401  (raises ImportError when the library is missing)
 from ._lib import KVError, SIGNATURES, lib  # noqa: F401
-from .cache import PagedKVCache  # noqa: F401
+from .cache import DeviceTables, PagedKVCache  # noqa: F401
 
-__all__ = ["PagedKVCache", "KVError", "lib", "SIGNATURES"]
+__all__ = ["PagedKVCache", "DeviceTables", "KVError", "lib", "SIGNATURES"]

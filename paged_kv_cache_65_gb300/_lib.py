@@ -44,6 +44,8 @@ KV_DEV_BAD_COW_PAIR = 4
 KV_DEV_WAIT_TIMEOUT = 8
 KV_DEV_BAD_CONTEXT = 16
 KV_DEV_SMEM_ALIGN = 32
+KV_DEV_NO_FREE_BLOCK = 64
+KV_DEV_BAD_TABLE_ROW = 128
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(
@@ -57,6 +59,14 @@ _i64p = C.POINTER(C.c_int64)
 _ip = C.POINTER(C.c_int)
 _vp = C.c_void_p
 _f32p = C.POINTER(C.c_float)
+
+
+class kvTables(C.Structure):
+    _fields_ = [("tables", _vp), ("lens", _vp), ("free_ids", _vp), ("free_state", _vp),
+                ("n_rows", C.c_int), ("max_blocks", C.c_int), ("free_cap", C.c_int)]
+
+
+_tp = C.POINTER(kvTables)
 
 # (name, restype, argtypes): every symbol declared in include/pagedkv.h
 SIGNATURES = [
@@ -98,6 +108,10 @@ SIGNATURES = [
                                      _vp]),
     ("paged_decode_attention", C.c_int, [_vp, C.c_int, _vp, C.c_int, _vp, C.c_int, _vp, C.c_int,
                                          C.c_float, _vp, C.c_int, _vp, C.c_size_t, _vp]),
+    ("paged_tables_workspace_bytes", C.c_size_t, [_vp, C.c_int]),
+    ("paged_tables_append", C.c_int, [_vp, _tp, _vp, _vp, C.c_int, C.c_int, _vp, _vp, _vp, _vp, _vp,
+                                      _vp, _vp, _vp, C.c_size_t, _vp]),
+    ("paged_tables_release", C.c_int, [_vp, _tp, _vp, C.c_int, _vp, C.c_size_t, _vp]),
     ("paged_decode_plan_bytes", C.c_size_t, [_vp, C.c_int, C.c_int]),
     ("paged_decode_plan", C.c_int, [_vp, _i32p, C.c_int, C.c_int, C.c_int, C.c_int, _vp,
                                     C.c_size_t, C.POINTER(C.c_size_t)]),

@@ -256,6 +256,29 @@ class PagedKVCache:
                                          _nbytes(workspace), _stream(stream)),
               "paged_decode_attention")
 
+    def paged_tables_workspace_bytes(self, n_seq):
+        return int(lib.paged_tables_workspace_bytes(self.handle, int(n_seq)))
+
+    def paged_tables_append(self, tables, d_rows, d_counts, n_seq, max_tokens, slots=None,
+                            positions=None, chunk_start=None, block_table=None, context_lens=None,
+                            lens_out=None, free_state_out=None, workspace=None, stream=None):
+        """Append the listed rows' new tokens (``d_counts``; None: one each)
+        to the ``DeviceTables``: blocks, slots, positions, compact table and
+        lengths, all on the device."""
+        check(lib.paged_tables_append(self.handle, tables.ref, vp(d_rows), vp(d_counts), int(n_seq),
+                                      int(max_tokens), vp(slots), vp(positions), vp(chunk_start),
+                                      vp(block_table), vp(context_lens), vp(lens_out),
+                                      vp(free_state_out), vp(workspace),
+                                      _nbytes(workspace) if workspace is not None else 0,
+                                      _stream(stream)), "paged_tables_append")
+
+    def paged_tables_release(self, tables, d_rows, n_seq, workspace=None, stream=None):
+        """Return the listed rows' blocks to the ring and empty the rows."""
+        check(lib.paged_tables_release(self.handle, tables.ref, vp(d_rows), int(n_seq),
+                                       vp(workspace),
+                                       _nbytes(workspace) if workspace is not None else 0,
+                                       _stream(stream)), "paged_tables_release")
+
     def paged_decode_plan(self, seq_ids, n_q_heads, max_blocks, min_shared_tokens=0):
         """Host plan of a sharing-aware decode pass: (plan bytes, workspace bytes)."""
         ids = i32(seq_ids)
@@ -366,8 +389,8 @@ class PagedKVCache:
                                        d_chunk_start, d_context_lens, n_seq, out, workspace,
                                        max_chunk=0, d_sched=None, n_items=0, scale=0.0,
                                        stream=None):
-        """Chunked prefill for any pool dtype (an FP8 pool through a bfloat16
-        copy in ``workspace``); natural grid over ``max_chunk``, or the work
+        """Chunked prefill for any pool dtype (an FP8 or q4_0 pool through a
+        16-bit copy in ``workspace``); natural grid over ``max_chunk``, or the work
         order ``d_sched`` of ``n_items`` records."""
         check(lib.paged_prefill_attention_staged(
             self.handle, int(layer), vp(q), int(n_q_heads), vp(d_table), int(max_blocks),
@@ -413,6 +436,45 @@ class PagedKVCache:
             self._stream_fn = (lambda: raw(dev)) if raw is not None else \
                 (lambda: torch.cuda.current_stream(dev).cuda_stream)
         return self._stream_fn()
+
+
+class DeviceTables:
+    """A set of block tables on the device (``kvTables``): int32 ``tables
+    [n_rows, max_blocks]``, ``lens [n_rows]``, the ring ``free_ids [free_cap]``
+    and int64 ``free_state [2]`` (oldest id's position, count)."""
+
+    def __init__(self, tables, lens, free_ids, free_state):
+        import torch
+
+        for t, dt, dim in ((tables, torch.int32, 2), (lens, torch.int32, 1),
+                           (free_ids, torch.int32, 1), (free_state, torch.int64, 1)):
+            if t.dtype != dt or t.dim() != dim or not t.is_contiguous():
+                raise TypeError("device tables: contiguous int32 tables [n_rows, max_blocks], "
+                                "lens, free_ids and int64 free_state")
+        if lens.numel() != tables.shape[0] or free_state.numel() != 2:
+            raise ValueError("device tables: one length per row, two ring numbers")
+        self.tables, self.lens = tables, lens
+        self.free_ids, self.free_state = free_ids, free_state
+        self._struct = _lib.kvTables(tables.data_ptr(), lens.data_ptr(), free_ids.data_ptr(),
+                                     free_state.data_ptr(), tables.shape[0], tables.shape[1],
+                                     free_ids.numel())
+        self.ref = C.byref(self._struct)
+
+    @classmethod
+    def from_pool(cls, cache, n_rows, max_blocks, n_blocks):
+        """Empty tables whose ring holds ``n_blocks`` blocks taken from the
+        pool (``block_alloc``; the tables hold the handles: give them back
+        with ``cache.block_free(tables.held)``)."""
+        import torch
+
+        held = cache.block_alloc(n_blocks)
+        dev = cache.k.device
+        t = cls(torch.full((n_rows, max_blocks), -1, dtype=torch.int32, device=dev),
+                torch.zeros(n_rows, dtype=torch.int32, device=dev),
+                torch.from_numpy(held).to(dev),
+                torch.tensor([0, n_blocks], dtype=torch.int64, device=dev))
+        t.held = held
+        return t
 
 
 def _addr(x) -> int:

@@ -69,6 +69,11 @@ struct PrefillArgs;
 cudaError_t launch_prefill_tc(const CUtensorMap& tk, const CUtensorMap& tv, const PrefillArgs& a,
                               int max_chunk, int n_items, cudaStream_t st, bool pdl);
 
+// The same over an fp16 copy of a q4_0 pool (a.seq_scale).
+cudaError_t launch_prefill_tc_f16(const CUtensorMap& tk, const CUtensorMap& tv,
+                                  const PrefillArgs& a, int max_chunk, int n_items,
+                                  cudaStream_t st, bool pdl);
+
 // tcgen05 variant (bfloat16, D_h = 128, the swizzled TMA maps); one CTA per SM.
 cudaError_t launch_tc_bf16(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeArgs& a,
                            int sm_count, int max_grid, int* grid_io, cudaStream_t st, bool pdl);

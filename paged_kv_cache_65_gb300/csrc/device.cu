@@ -635,19 +635,26 @@ WsLayout ws_layout(const kvPool* p, int n_seq, int G) {
 bool aligned16(const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15) == 0; }
 
 // Checks and launch shared by the natural-grid and the scheduled prefill.
-// Staged prefill of an FP8 pool: the bfloat16 copy the attention reads
-// instead of the pool (its TMA descriptors, its table, its block count).
+// Staged prefill of an FP8 or q4_0 pool: the bfloat16 (q4_0: fp16) copy the
+// attention reads instead of the pool (its TMA descriptors, its table, its
+// block count; q4_0: the copies' powers of two).
 struct PrefillStage {
   const CUtensorMap* tk;
   const CUtensorMap* tv;
   const int32_t* table;
   int n_blocks;
+  const float2* seq_scale;
 };
 
+// Pools whose chunked prefill reads a copy.
+bool prefill_staged(const kvPool* p) {
+  return p->dtype == KV_DTYPE_FP8_E4M3 || p->dtype == KV_DTYPE_Q4_0;
+}
+
 // Whether a pool can run the chunked-prefill pass: bfloat16 in place, or
-// FP8 (D_h = 128, the tensor-core block shapes) through a bfloat16 copy.
+// FP8 / q4_0 (D_h = 128, the tensor-core block shapes) through a copy.
 bool prefill_shape(const kvPool* p, bool staged) {
-  return staged ? p->dtype == KV_DTYPE_FP8_E4M3 && p->D == 128 && pool_tensor_core_shape(p)
+  return staged ? prefill_staged(p) && p->D == 128 && pool_tensor_core_shape(p)
                 : pool_tc_shape(p);
 }
 
@@ -693,11 +700,14 @@ kvStatus prefill_common(kvPool* p, int layer, const void* d_q, int n_q_heads,
   // V's scales the outputs
   a.qscale = scale * 1.4426950408889634f * (stage ? p->k_scale : 1.f);  // log2(e)
   a.vscale = stage ? p->v_scale : 1.f;
+  a.seq_scale = stage ? stage->seq_scale : nullptr;
   const CUtensorMap& tk = stage ? *stage->tk : *reinterpret_cast<const CUtensorMap*>(p->tmap[2]);
   const CUtensorMap& tv = stage ? *stage->tv : *reinterpret_cast<const CUtensorMap*>(p->tmap[3]);
+  const bool pdl = p->pdl && !p->device_tables;  // as in paged_decode_partials
   const cudaError_t e =
-      pkv::launch_prefill_tc(tk, tv, a, max_chunk, n_items, as_stream(stream),
-                             p->pdl && !p->device_tables);
+      p->dtype == KV_DTYPE_Q4_0
+          ? pkv::launch_prefill_tc_f16(tk, tv, a, max_chunk, n_items, as_stream(stream), pdl)
+          : pkv::launch_prefill_tc(tk, tv, a, max_chunk, n_items, as_stream(stream), pdl);
   return e == cudaSuccess ? KV_OK : KV_ERR_CUDA;
 }
 
@@ -1280,11 +1290,12 @@ kvStatus paged_prefill_attention_scheduled(kvPool* p, int layer, const void* d_q
 }
 
 namespace {
-// Workspace of a staged prefill: bfloat16 copies of K and V as rows
-// (copy block, slot) of H_kv * D_h values, then the copy's table.
+// Workspace of a staged prefill: 16-bit copies of K and V as rows (copy
+// block, slot) of H_kv * D_h values, then the copy's table and, for a q4_0
+// pool, the copies' powers of two per (sequence, K/V head).
 struct StageLayout {
   long long rows;
-  size_t k, v, table, total;
+  size_t k, v, table, scale, total;
 };
 StageLayout stage_layout(const kvPool* p, int n_seq, int max_blocks) {
   StageLayout l;
@@ -1293,13 +1304,16 @@ StageLayout stage_layout(const kvPool* p, int n_seq, int max_blocks) {
   l.k = 0;
   l.v = kv;
   l.table = 2 * kv;
-  l.total = l.table + align256(static_cast<size_t>(n_seq) * max_blocks * sizeof(int32_t));
+  l.scale = l.table + align256(static_cast<size_t>(n_seq) * max_blocks * sizeof(int32_t));
+  l.total = l.scale + (p->dtype == KV_DTYPE_Q4_0
+                           ? align256(static_cast<size_t>(n_seq) * p->H * sizeof(float2))
+                           : 0);
   return l;
 }
 }  // namespace
 
 size_t paged_prefill_staging_bytes(const kvPool* p, int n_seq, int max_blocks) {
-  if (!p || n_seq < 0 || max_blocks <= 0 || p->dtype != KV_DTYPE_FP8_E4M3) return 0;
+  if (!p || n_seq < 0 || max_blocks <= 0 || !prefill_staged(p)) return 0;
   return stage_layout(p, n_seq, max_blocks).total;
 }
 
@@ -1313,7 +1327,7 @@ kvStatus paged_prefill_attention_staged(kvPool* p, int layer, const void* d_q, i
   if (!p || !p->k || n_seq < 0 || max_chunk < 0 || n_items < 0) return KV_ERR_INVALID_ARG;
   if (d_sched && !aligned16(d_sched)) return KV_ERR_INVALID_ARG;
   const int4* sched = static_cast<const int4*>(d_sched);
-  if (p->dtype != KV_DTYPE_FP8_E4M3)  // read in place
+  if (!prefill_staged(p))  // read in place
     return prefill_common(p, layer, d_q, n_q_heads, d_block_table, max_blocks, d_chunk_start,
                           d_context_lens, n_seq, sched ? 0 : max_chunk, sched, n_items, scale,
                           d_out, out_dtype, stream);
@@ -1333,7 +1347,12 @@ kvStatus paged_prefill_attention_staged(kvPool* p, int layer, const void* d_q, i
   unsigned char* w = static_cast<unsigned char*>(d_workspace);
   int32_t* stage_table = reinterpret_cast<int32_t*>(w + l.table);
   const int row_vecs = p->H * p->D / 16;
-  const cudaError_t e = pkv::launch_kernel(
+  float2* seq_scale =
+      p->dtype == KV_DTYPE_Q4_0 ? reinterpret_cast<float2*>(w + l.scale) : nullptr;
+  const pkv::StageQ4 q4{d_block_table, d_context_lens, n_seq, max_blocks, layer, w + l.k, w + l.v,
+                        stage_table, seq_scale};
+  const cudaError_t e = seq_scale ? pkv::launch_prefill_stage_q4(p, q4, as_stream(stream))
+                                  : pkv::launch_kernel(
       p->pdl, prefill_stage_fp8_kernel, dim3(max_blocks, n_seq), dim3(128), 0, as_stream(stream),
       reinterpret_cast<const uint4*>(p->k), reinterpret_cast<const uint4*>(p->v), d_block_table,
       d_context_lens, max_blocks, layer, p->N, p->B, row_vecs, reinterpret_cast<uint4*>(w + l.k),
@@ -1345,7 +1364,9 @@ kvStatus paged_prefill_attention_staged(kvPool* p, int layer, const void* d_q, i
     for (int kv = 0; kv < 2; ++kv) {
       s = encode_rows_map(w + (kv ? l.v : l.k), static_cast<unsigned long long>(l.rows),
                           static_cast<unsigned long long>(p->H) * p->D, 2,
-                          CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 64, rm, true,
+                          seq_scale ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                    : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                          64, rm, true,
                           reinterpret_cast<CUtensorMap*>(p->tmap_stage[kv]));
       if (s != KV_OK) {
         p->stage_base = nullptr;
@@ -1357,7 +1378,7 @@ kvStatus paged_prefill_attention_staged(kvPool* p, int layer, const void* d_q, i
   }
   const PrefillStage st{reinterpret_cast<const CUtensorMap*>(p->tmap_stage[0]),
                         reinterpret_cast<const CUtensorMap*>(p->tmap_stage[1]), stage_table,
-                        n_seq * max_blocks};
+                        n_seq * max_blocks, seq_scale};
   return prefill_common(p, layer, d_q, n_q_heads, d_block_table, max_blocks, d_chunk_start,
                         d_context_lens, n_seq, sched ? 0 : max_chunk, sched, n_items, scale,
                         d_out, out_dtype, stream, &st);

@@ -22,6 +22,9 @@ struct PrefillArgs {
   int n_seq, max_blocks, layer, n_blocks, block_size, n_kv_heads, n_q_heads;
   float qscale;  // scale * log2(e) (times the K scale of an FP8 pool's codes)
   float vscale;  // factor of the outputs: 1, or the V scale of an FP8 pool's codes
+  // fp16 variant: per (sequence, K/V head) the powers of two (K's, V's) that
+  // the staged copies were divided by
+  const float2* seq_scale;
 };
 
 }  // namespace pkv

@@ -37,6 +37,15 @@
 // ~60 cycles, about the tensor core's time for one 128 x 128 x 16 step).
 // Every mbarrier wait is bounded; parity waits are exact because no waiter
 // runs two phases ahead.
+//
+// F16: K and V are an fp16 copy of a q4_0 pool, scaled per (sequence, K/V
+// head) by a power of two (prefill_stage_q4_kernel).  q is turned into fp16
+// on the way into shared memory, each row scaled by the power of two that
+// brings its largest |q| into [2^11, 2^12) (bf16's 8 bits stay exact over 2^25
+// of range), and both factors join the row's score scale.  P is fp16 with 11
+// significant bits, one operand instead of two: p <= 2^8 by the lazy
+// reference, so it stays in fp16's range, and the P.V product takes half the
+// MMAs.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -113,6 +122,7 @@ __device__ __forceinline__ uint32_t kmajor_chunk(uint32_t base, int r, int ch) {
   return base + (ch >> 3) * (128 * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
 }
 
+template <bool F16>
 __global__ void __launch_bounds__(kPfThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k,
                       const __grid_constant__ CUtensorMap tmap_v, const PrefillArgs a) {
@@ -220,7 +230,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     if (lane == 0) prefetch_tmap(tmap);
     TableCacheN<kPfTableCache> tc;
     tc.ent = tcache + (warp - 8) * kPfTableCache;
-    tc.ensure(a.table, a.max_blocks, s, 0, 0, lane);  // host-written: before the wait
+    // host-written: before the wait (F16: the copy's table, which the kernel
+    // before this one writes, is read after it)
+    if constexpr (!F16) tc.ensure(a.table, a.max_blocks, s, 0, 0, lane);
     griddep_wait();
     griddep_launch_dependents();
     bool alive = true;
@@ -276,7 +288,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         // S of block j into S/P buffer j % NSB, once K has landed and the
         // P.V that last read the buffer (block j - NSB) is done
         const uint32_t qb = smem_u32(q_s), kb = smem_u32(k_st);
-        constexpr uint32_t idS = idesc_bf16(128, 128, false, false);
+        constexpr uint32_t idS =
+            F16 ? idesc_f16(128, 128, false, false) : idesc_bf16(128, 128, false, false);
         wait(q_full, 0);
         for (int j = 0; j < n_kb && alive; ++j) {
           if (!wait(&k_full[j % NST], (j / NST) & 1)) break;
@@ -294,7 +307,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         }
       } else {
         const uint32_t vb = smem_u32(v_st);
-        constexpr uint32_t idPV = idesc_bf16(128, 128, false, true);
+        constexpr uint32_t idPV =
+            F16 ? idesc_f16(128, 128, false, true) : idesc_bf16(128, 128, false, true);
         for (int j = 0; j < n_kb && alive; ++j) {
           wait(&p_full[j % C::NSB], (j / C::NSB) & 1);
           wait(&v_full[j % NST], (j / NST) & 1);
@@ -307,7 +321,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           for (int k = 0; k < nk; ++k) {
             const uint64_t dv = smem_desc(vs + k * 2048, C::HALF, 1024, kSwizzle128);
             tc_mma_ts(tmem + C::TM_O, pt + k * 8, dv, idPV, (j > 0 || k > 0) ? 1u : 0u);
-            tc_mma_ts(tmem + C::TM_O, pt + 64 + k * 8, dv, idPV, 1u);
+            if constexpr (!F16) tc_mma_ts(tmem + C::TM_O, pt + 64 + k * 8, dv, idPV, 1u);
           }
           tc_commit(&v_empty[j % NST]);
         }
@@ -339,22 +353,55 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     };
     // ---- Q tile: row r, K-major, 128-byte swizzle (zero past the chunk);
     // each half stages its 64 dimensions
+    float qs = a.qscale;
     {
       const uint32_t qbase = smem_u32(q_s);
       const uint4* src = reinterpret_cast<const uint4*>(
           reinterpret_cast<const unsigned char*>(a.q) +
           ((static_cast<long long>(row0 + tok0 + tl) * a.n_q_heads + head * G + g) * C::D) * 2);
+      if constexpr (F16) {
+        uint4 v[8];
+        uint32_t am = 0;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          v[c] = row_ok ? src[8 * hh + c] : make_uint4(0, 0, 0, 0);
+          const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            am = max(am, max((w[i] << 16) & 0x7fffffffu, w[i] & 0x7fff0000u));
+        }
+        // the row's largest exponent over both halves, through the exchange
+        // slots of the parity the first block does not use
+        uint16_t* xq = xmax + 256;
+        xq[hh * 128 + r] = static_cast<uint16_t>(am >> 23);
+        named_bar_sync(xbar, 64);
+        int E = max(static_cast<int>(am >> 23), static_cast<int>(xq[(1 - hh) * 128 + r]));
+        E = E < 12 ? 12 : E;
+        const float sc = __uint_as_float(static_cast<uint32_t>(265 - E) << 23);  // 2^(138 - E)
+        qs *= a.seq_scale[s * H + head].x * __uint_as_float(static_cast<uint32_t>(E) << 23) *
+              0x1p-11f;  // 2^(E - 138)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+          uint32_t f[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            f[i] = pack_f16(__uint_as_float(w[i] << 16) * sc,
+                            __uint_as_float(w[i] & 0xffff0000u) * sc);
+          sts128(kmajor_chunk(qbase, r, 8 * hh + c), f[0], f[1], f[2], f[3]);
+        }
+      } else {
 #pragma unroll 4
       for (int c = 0; c < 8; ++c) {
         const int ch = 8 * hh + c;
         const uint4 v = row_ok ? src[ch] : make_uint4(0, 0, 0, 0);
         sts128(kmajor_chunk(qbase, r, ch), v.x, v.y, v.z, v.w);
       }
+      }
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
     }
-    const float qs = a.qscale;
     float m_ref = -INFINITY, l = 0.f;  // l: this half's sum
     for (int j = 0; j < n_kb; ++j) {
       const int slot = j % NST;
@@ -449,6 +496,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           const float p0 = exp2_approx(x0), p1 = exp2_approx(x1);
           const uint64_t pp = f2_pack(p0, p1);
           lp2[k & 1] = f2_add(lp2[k & 1], pp);
+          if constexpr (F16) {
+            hi[k] = pack_f16(p0, p1);
+            continue;
+          }
           const uint32_t b0 = __float_as_uint(p0), b1 = __float_as_uint(p1);
           hi[k] = __byte_perm(b0, b1, 0x7632);
           float r0, r1;
@@ -459,7 +510,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           lo[k] = __byte_perm(__float_as_uint(r0), __float_as_uint(r1), 0x7632);
         }
         tmem_st32_nowait(sb + 32 * hh, hi);
-        tmem_st32_nowait(sb + 64 + 32 * hh, lo);
+        if constexpr (!F16) tmem_st32_nowait(sb + 64 + 32 * hh, lo);
       }
       {
         float a0, a1, b0, b1;
@@ -504,7 +555,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     wait(&v_empty[(n_kb - 1) % NST], ((n_kb - 1) / NST) & 1);
     __syncwarp();
     tc_fence_after();
-    const float inv = lt > 0.f ? a.vscale / lt : 0.f;
+    const float vscale = F16 ? a.seq_scale[s * H + head].y : a.vscale;
+    const float inv = lt > 0.f ? vscale / lt : 0.f;
     const long long orow = (static_cast<long long>(row0 + tok0 + tl) * a.n_q_heads + head * G + g);
 #pragma unroll 1
     for (int c0 = 64 * hh; c0 < 64 * hh + 64; c0 += 32) {

@@ -1,0 +1,13 @@
+// The tcgen05 chunked-prefill attention over an fp16 copy of a q4_0 pool,
+// D_h = 128.
+#include "prefill_tc_launch.cuh"
+
+namespace pkv {
+
+cudaError_t launch_prefill_tc_f16(const CUtensorMap& tk, const CUtensorMap& tv,
+                                  const PrefillArgs& a, int max_chunk, int n_items,
+                                  cudaStream_t st, bool pdl) {
+  return launch_prefill<true>(tk, tv, a, max_chunk, n_items, st, pdl);
+}
+
+}  // namespace pkv

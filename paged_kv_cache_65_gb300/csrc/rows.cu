@@ -187,7 +187,141 @@ cudaError_t launch_gather(const kvPool* p, int layer, const int64_t* slots, int 
                        v_out, p->d_status);
 }
 
+// Staged chunked prefill of a q4_0 pool, first kernel: one CTA per (K/V head,
+// sequence) finds the largest K and V scale inside the sequence's context and
+// from it the power of two 2^e that the copies are divided by: with
+// d < 2^(floor(log2 d) + 1), |c d| < 2^(floor(log2 d) + 4), so e =
+// floor(log2 d) - 11 keeps every copied value below 2^15 and the values down
+// to 2^-29 of that normal in fp16, whatever the magnitude of K and V.  Reads
+// the scales alone (a ninth of the blocks' bytes).
+constexpr int kScaleThreads = 512;
+
+__global__ void __launch_bounds__(kScaleThreads)
+    prefill_scale_q4_kernel(const unsigned char* __restrict__ kc,
+                            const unsigned char* __restrict__ vc, StageQ4 g, int n_blocks, int B,
+                            int H, int GR) {
+  __shared__ uint32_t red[2][kScaleThreads / 32];
+  const int h = blockIdx.x, i = blockIdx.y;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int len = g.ctx[i];
+  const long long chunk_bytes = static_cast<long long>(B) * GR * 18;
+  const int vecs = B * GR / 8;  // 16-byte vectors of a chunk's scales
+  int nb = len > 0 ? (len + B - 1) / B : 0;
+  if (nb > g.max_blocks) nb = g.max_blocks;
+  uint32_t mk = 0, mv = 0;
+  const long long total = static_cast<long long>(nb) * vecs;
+  for (long long w = threadIdx.x; w < total; w += kScaleThreads) {
+    const int j = static_cast<int>(w / vecs), v = static_cast<int>(w - static_cast<long long>(j) * vecs);
+    const int pid = g.table[static_cast<long long>(i) * g.max_blocks + j];
+    if (pid < 0 || pid >= n_blocks) continue;  // flagged by the copy
+    const long long off = ((static_cast<long long>(g.layer) * n_blocks + pid) * H + h) * chunk_bytes +
+                          static_cast<long long>(GR) * B * 16;
+    const uint4 xk = reinterpret_cast<const uint4*>(kc + off)[v];
+    const uint4 xv = reinterpret_cast<const uint4*>(vc + off)[v];
+    const uint32_t wk[4] = {xk.x, xk.y, xk.z, xk.w}, wv[4] = {xv.x, xv.y, xv.z, xv.w};
+    const int rows = len - j * B;  // slots of this block inside the context
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int o = v * 8 + e;
+      const uint32_t bk = (wk[e >> 1] >> (16 * (e & 1))) & 0x7fffu;
+      const uint32_t bv = (wv[e >> 1] >> (16 * (e & 1))) & 0x7fffu;
+      if (o / GR < rows) mk = max(mk, bk);  // K: [B][GR]
+      if (o % B < rows) mv = max(mv, bv);   // V: [GR][B]
+    }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    mk = max(mk, __shfl_xor_sync(0xffffffffu, mk, o));
+    mv = max(mv, __shfl_xor_sync(0xffffffffu, mv, o));
+  }
+  if ((threadIdx.x & 31) == 0) {
+    red[0][threadIdx.x >> 5] = mk;
+    red[1][threadIdx.x >> 5] = mv;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 0; w < kScaleThreads / 32; ++w) {
+      mk = max(mk, red[0][w]);
+      mv = max(mv, red[1][w]);
+    }
+    auto pow2 = [](uint32_t bits) {
+      const float d = __half2float(__ushort_as_half(static_cast<unsigned short>(bits)));
+      const int e = static_cast<int>(__float_as_uint(d) >> 23) - 127;  // floor(log2 d)
+      return bits == 0 ? 1.f : __uint_as_float(static_cast<uint32_t>(e - 11 + 127) << 23);
+    };
+    g.seq_scale[i * H + h] = make_float2(pow2(mk), pow2(mv));
+  }
+}
+
+// Second kernel: the codes of every block a listed sequence reads become fp16
+// values c d / 2^e (c d is exact in float32; one rounding, 2^-11 relative),
+// logical block j of sequence i at copy block i * max_blocks + j; slots past
+// the context are zeros.  One CTA per (logical block, sequence); neighbouring
+// lanes take the groups of one (slot, head), adjacent in the copy.
+__global__ void __launch_bounds__(256)
+    prefill_stage_q4_kernel(const unsigned char* __restrict__ kc,
+                            const unsigned char* __restrict__ vc, StageQ4 g, int n_blocks, int B,
+                            int H, int GR, int32_t* status) {
+  const int j = blockIdx.x, i = blockIdx.y;
+  const long long sb = static_cast<long long>(i) * g.max_blocks + j;
+  griddep_wait();
+  griddep_launch_dependents();
+  if (threadIdx.x == 0) g.stage_table[sb] = static_cast<int32_t>(sb);
+  const int len = g.ctx[i];
+  if (len <= 0 || j >= (len + B - 1) / B) return;
+  const int pid = g.table[sb];
+  const bool ok = pid >= 0 && pid < n_blocks;
+  if (!ok && threadIdx.x == 0) record_status(status, KV_DEV_BAD_BLOCK_ID);
+  const int rows = len - j * B < B ? len - j * B : B;
+  const long long chunk_bytes = static_cast<long long>(B) * GR * 18;
+  const long long blk = (static_cast<long long>(g.layer) * n_blocks + (ok ? pid : 0)) * H;
+  const int n = B * H * GR;  // groups of one of K, V
+  for (int idx = threadIdx.x; idx < 2 * n; idx += blockDim.x) {
+    const bool is_k = idx < n;
+    const int x = is_k ? idx : idx - n;
+    const int q = x % GR, h = x / GR % H, o = x / (GR * H);
+    uint4 out[4] = {};
+    if (ok && o < rows) {
+      const unsigned char* chunk = (is_k ? kc : vc) + (blk + h) * chunk_bytes;
+      const uint4 c =
+          *reinterpret_cast<const uint4*>(chunk + (static_cast<long long>(q) * B + o) * 16);
+      const float2 e = g.seq_scale[i * H + h];
+      const __half* sc = reinterpret_cast<const __half*>(chunk + static_cast<long long>(GR) * B * 16);
+      const float d = __half2float(sc[is_k ? o * GR + q : q * B + o]) / (is_k ? e.x : e.y);
+      const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t h2[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const float lo = d * static_cast<float>(static_cast<int>((w[k] >> (8 * b)) & 15u) - 8);
+          const float hi = d * static_cast<float>(static_cast<int>((w[k] >> (8 * b + 4)) & 15u) - 8);
+          const __half2 p = __floats2half2_rn(lo, hi);
+          h2[b] = *reinterpret_cast<const uint32_t*>(&p);
+        }
+        out[k] = make_uint4(h2[0], h2[1], h2[2], h2[3]);
+      }
+    }
+    uint4* dst = static_cast<uint4*>(is_k ? g.k_stage : g.v_stage) +
+                 ((sb * B + o) * H + h) * (GR * 4) + q * 4;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) dst[k] = out[k];
+  }
+}
+
 }  // namespace
+
+cudaError_t launch_prefill_stage_q4(const kvPool* p, const StageQ4& g, cudaStream_t st) {
+  const unsigned char* kc = static_cast<const unsigned char*>(p->k);
+  const unsigned char* vc = static_cast<const unsigned char*>(p->v);
+  const cudaError_t e =
+      launch_kernel(p->pdl, prefill_scale_q4_kernel, dim3(p->H, g.n_seq), dim3(kScaleThreads), 0,
+                    st, kc, vc, g, p->N, p->B, p->H, p->D / 32);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(p->pdl, prefill_stage_q4_kernel, dim3(g.max_blocks, g.n_seq), dim3(256), 0,
+                       st, kc, vc, g, p->N, p->B, p->H, p->D / 32, p->d_status);
+}
 
 cudaError_t launch_slot_write_q4(const kvPool* p, int layer, const void* k_new, const void* v_new,
                                  const int64_t* slots, int n_tokens, cudaStream_t st) {

@@ -17,4 +17,17 @@ cudaError_t launch_slot_write_q4(const kvPool* p, int layer, const void* k_new, 
 cudaError_t launch_gather_rows(const kvPool* p, int layer, const int64_t* slots, int n_tokens,
                                void* k_out, void* v_out, int out_dtype, cudaStream_t st);
 
+// fp16 copy of the blocks a staged prefill of a q4_0 pool reads: first the
+// (sequence, K/V head) powers of two (seq_scale), then the copy.
+struct StageQ4 {
+  const int32_t* table;  // [n_seq][max_blocks]
+  const int32_t* ctx;    // [n_seq]
+  int n_seq, max_blocks, layer;
+  void* k_stage;         // fp16 rows (copy block i * max_blocks + j, slot) of H_kv * D_h
+  void* v_stage;
+  int32_t* stage_table;  // [n_seq][max_blocks]: i * max_blocks + j
+  float2* seq_scale;     // [n_seq][H_kv]
+};
+cudaError_t launch_prefill_stage_q4(const kvPool* p, const StageQ4& g, cudaStream_t st);
+
 }  // namespace pkv

@@ -14,7 +14,73 @@ from __future__ import annotations
 import numpy as np
 import torch
 
-from .cache import PagedKVCache
+from .cache import DeviceTables, PagedKVCache
+
+
+class TableRun:
+    """Prefill rounds and decode steps of requests whose block tables live on
+    the device (``DeviceTables``): every call appends the requests' tokens to
+    their rows, writes the new K/V and attends, with no host reservation, no
+    upload and no synchronisation, so a captured step can be replayed.
+
+    ``rows``: int32 device tensor of table rows (-1: a padding entry); new K/V
+    ``[L, n_tokens, H_kv, D_h]`` and q ``[L, n_tokens, H_q, D_h]`` device
+    tensors of the pool's input dtype, the batch's tokens in row order."""
+
+    def __init__(self, cache: PagedKVCache, n_q_heads, n_rows, max_blocks, n_blocks, max_batch,
+                 max_tokens=0):
+        self.c, self.n_q_heads, self.mb = cache, n_q_heads, max_blocks
+        self.t = DeviceTables.from_pool(cache, n_rows, max_blocks, n_blocks)
+        dev, mt = cache.k.device, max(max_tokens, max_batch)
+        i32 = dict(dtype=torch.int32, device=dev)
+        self.slots = torch.empty(mt, dtype=torch.int64, device=dev)
+        self.positions = torch.empty(mt, **i32)
+        self.start = torch.empty(max_batch + 1, **i32)
+        self.table = torch.empty((max_batch, max_blocks), **i32)
+        self.lens = torch.empty(max_batch, **i32)
+        u8 = dict(dtype=torch.uint8, device=dev)
+        self._ws = torch.empty(cache.paged_tables_workspace_bytes(max_batch), **u8)
+        self._attn = torch.empty(cache.paged_decode_workspace_bytes(max_batch, n_q_heads), **u8)
+        stage = cache.paged_prefill_staging_bytes(max_batch, max_blocks) if max_tokens else 0
+        self._stage = torch.empty(stage, **u8) if stage else None
+
+    def _append(self, rows, counts, n_tokens, stream):
+        n = rows.numel()
+        self.c.paged_tables_append(self.t, rows, counts, n, n_tokens, self.slots, self.positions,
+                                   self.start, self.table, self.lens, workspace=self._ws,
+                                   stream=stream)
+        return n
+
+    def prefill(self, rows, counts, max_chunk, q, k_new, v_new, out, stream=None):
+        """Append ``counts`` tokens (int32, at most ``max_chunk`` each) to the
+        rows and attend them over their contexts; ``out [L, n_tokens, H_q,
+        D_h]``, rows past the last token left as they were."""
+        c, n_tok = self.c, k_new.shape[1]
+        n = self._append(rows, counts, n_tok, stream)
+        c.reshape_and_cache(-1, k_new, v_new, self.slots, n_tok, stream)
+        for layer in range(c.L):
+            c.paged_prefill_attention_staged(layer, q[layer], self.n_q_heads, self.table, self.mb,
+                                             self.start, self.lens, n, out[layer], self._stage,
+                                             max_chunk=max_chunk, stream=stream)
+        return out
+
+    def step(self, rows, q, k_new, v_new, out, stream=None):
+        """One decode step: a token for every listed row, padding entries last;
+        ``out [L, n, H_q, D_h]``, zeros for padding entries."""
+        c = self.c
+        n = self._append(rows, None, rows.numel(), stream)
+        c.reshape_and_cache(-1, k_new, v_new, self.slots, n, stream)
+        for layer in range(c.L):
+            c.paged_decode_attention(layer, q[layer], self.n_q_heads, self.table, self.mb,
+                                     self.lens, n, out[layer], self._attn, 0.0, stream)
+        return out
+
+    def release(self, rows, stream=None):
+        self.c.paged_tables_release(self.t, rows, rows.numel(), self._ws, stream)
+
+    def close(self):
+        """Give the ring's blocks back to the pool."""
+        self.c.block_free(self.t.held)
 
 
 def to_device(x: np.ndarray, dtype: str, device) -> torch.Tensor:
@@ -187,7 +253,7 @@ class DeviceRun:
             sched = c.paged_prefill_schedule(starts, d_lens.cpu().numpy(), self.n_q_heads)
             d_sched = torch.from_numpy(sched).to(self.dev)
         outs = []
-        staged = c.dtype == "fp8_e4m3"  # FP8 pools: through a bfloat16 copy
+        staged = c.dtype in ("fp8_e4m3", "q4_0")  # through a 16-bit copy
         if staged:
             nbytes = c.paged_prefill_staging_bytes(len(chunks), mb)
             if self._stage_ws is None or self._stage_ws.numel() < nbytes:
