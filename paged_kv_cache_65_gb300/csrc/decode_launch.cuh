@@ -104,6 +104,10 @@ cudaError_t launch_mma_q8(int D, int G, const CUtensorMap& tk, const CUtensorMap
 cudaError_t launch_decode_q4(int D, const DecodeArgs& a, int sm_count, int max_grid, int* grid_io,
                              cudaStream_t st, bool pdl, bool* supported);
 
+// The tcgen05 pass over a q4_0 pool, D_h = 128; one CTA per SM.
+cudaError_t launch_decode_q4_tc(const DecodeArgs& a, int sm_count, int max_grid, int* grid_io,
+                                cudaStream_t st, bool pdl);
+
 // Dispatch over (D, G) for one element size; *supported = false when the
 // shape has no compiled instantiation.
 cudaError_t launch_split_e2(int D, int G, const CUtensorMap& tk, const CUtensorMap& tv,

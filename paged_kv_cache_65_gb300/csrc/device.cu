@@ -431,21 +431,37 @@ __global__ void __launch_bounds__(128) merge_kernel(const long long* __restrict_
 #pragma unroll
       for (int off = 16; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
       float L = 0.f;
-      for (int i = 0; i < np; ++i) {
-        const long long slot = (c0 + i + seg) * G + g;
-        const float f = pkv::exp2_approx(ws_ml[slot * 2] - M);
-        L += f * ws_ml[slot * 2 + 1];
-        const float* src = ws_o + slot * D + lane * DL;
-        if constexpr (DL == 4) {
-          const float4 v = *reinterpret_cast<const float4*>(src);
-          o[0] += f * v.x;
-          o[1] += f * v.y;
-          o[2] += f * v.z;
-          o[3] += f * v.w;
-        } else {
-          const float2 v = *reinterpret_cast<const float2*>(src);
-          o[0] += f * v.x;
-          o[1] += f * v.y;
+      // eight pieces' loads in flight at a time, summed in piece order (a long
+      // context split over many CTAs has tens of them)
+      constexpr int kAhead = 8;
+      for (int i0 = 0; i0 < np; i0 += kAhead) {
+        float2 ml[kAhead];
+        float v[kAhead][DL];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          if (i0 + u >= np) continue;
+          const long long slot = (c0 + i0 + u + seg) * G + g;
+          ml[u] = *reinterpret_cast<const float2*>(&ws_ml[slot * 2]);
+          const float* src = ws_o + slot * D + lane * DL;
+          if constexpr (DL == 4) {
+            const float4 x = *reinterpret_cast<const float4*>(src);
+            v[u][0] = x.x;
+            v[u][1] = x.y;
+            v[u][2] = x.z;
+            v[u][3] = x.w;
+          } else {
+            const float2 x = *reinterpret_cast<const float2*>(src);
+            v[u][0] = x.x;
+            v[u][1] = x.y;
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          if (i0 + u >= np) continue;
+          const float f = pkv::exp2_approx(ml[u].x - M);
+          L += f * ml[u].y;
+#pragma unroll
+          for (int d = 0; d < DL; ++d) o[d] += f * v[u][d];
         }
       }
       const float inv = 1.f / L;
@@ -919,9 +935,15 @@ kvStatus paged_decode_partials(kvPool* p, int layer, const void* d_q, int n_q_he
   bool supported = false;
   cudaError_t e;
   if (p->dtype == KV_DTYPE_Q4_0) {
-    if (kern != kKernelMma) return KV_ERR_UNSUPPORTED;  // no CUDA-core pass over codes
-    e = pkv::launch_decode_q4(p->D, a, p->sm_count, kMaxDecodeCtas, grid_io, as_stream(stream),
-                              p->pdl, &supported);
+    if (kern == kKernelCudaCores) return KV_ERR_UNSUPPORTED;  // no CUDA-core pass over codes
+    if (kern == kKernelTc) {
+      e = pkv::launch_decode_q4_tc(a, p->sm_count, kMaxDecodeCtas, grid_io, as_stream(stream),
+                                   p->pdl);
+      supported = true;
+    } else {
+      e = pkv::launch_decode_q4(p->D, a, p->sm_count, kMaxDecodeCtas, grid_io, as_stream(stream),
+                                p->pdl, &supported);
+    }
   } else if (p->dtype == KV_DTYPE_FP8_E4M3 && kern == kKernelTc) {
     const CUtensorMap& tk = *reinterpret_cast<const CUtensorMap*>(p->tmap[2]);
     const CUtensorMap& tv = *reinterpret_cast<const CUtensorMap*>(p->tmap[3]);
@@ -1100,7 +1122,10 @@ kvStatus partials_planned(kvPool* p, int layer, const void* d_q, int n_q_heads,
   const CUtensorMap& tv = *reinterpret_cast<const CUtensorMap*>(p->tmap[3]);
   bool supported = true;
   const cudaError_t e =
-      tc ? (p->dtype == KV_DTYPE_FP8_E4M3
+      tc ? (p->dtype == KV_DTYPE_Q4_0
+                ? pkv::launch_decode_q4_tc(a, p->sm_count, kMaxDecodeCtas, &p->grid_tc,
+                                           as_stream(stream), p->pdl)
+            : p->dtype == KV_DTYPE_FP8_E4M3
                 ? pkv::launch_tc_fp8(tk, tv, a, p->sm_count, kMaxDecodeCtas, &p->grid_tc,
                                      as_stream(stream), pdl)
                 : pkv::launch_tc_bf16(tk, tv, a, p->sm_count, kMaxDecodeCtas, &p->grid_tc,

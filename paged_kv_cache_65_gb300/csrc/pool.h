@@ -133,9 +133,10 @@ inline bool pool_tc_shape(const kvPool* p) {
 
 // The tcgen05 decode pass: bfloat16 as above, or FP8 codes with D_h = 128
 // (converted to fp16 in the pass: K rows into tensor memory, V rows into
-// shared memory).
+// shared memory), or q4_0 with D_h = 128 (the same way).
 inline bool pool_tc_decode_shape(const kvPool* p) {
-  return (p->dtype == KV_DTYPE_BF16 || p->dtype == KV_DTYPE_FP8_E4M3) &&
+  return (p->dtype == KV_DTYPE_BF16 || p->dtype == KV_DTYPE_FP8_E4M3 ||
+          p->dtype == KV_DTYPE_Q4_0) &&
          pool_tensor_core_shape(p) && p->D == 128;
 }
 

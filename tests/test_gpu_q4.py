@@ -61,12 +61,16 @@ def same_pool(cache, st):
             and np.array_equal(vc, st.V) and np.array_equal(vs, st.Vs))
 
 
-def make(wl, fill=0):
-    from paged_kv_cache_65_gb300 import PagedKVCache
+MMA, TC = 2, 3  # KV_OPT_DECODE_PATH: the warp-level pass, the tcgen05 pass (D_h = 128)
+
+
+def make(wl, fill=0, path=0):
+    from paged_kv_cache_65_gb300 import PagedKVCache, _lib
     from paged_kv_cache_65_gb300.driver import DeviceRun
 
     cache = PagedKVCache(wl.n_layers, wl.n_blocks, wl.block_size, wl.n_kv_heads, wl.head_dim,
                          wl.dtype, free_order=wl.free_order)
+    cache.kv_pool_set_option(_lib.KV_OPT_DECODE_PATH, path)
     cache.k.fill_(fill)
     cache.v.fill_(fill)
     run = DeviceRun(cache, wl.n_q_heads)
@@ -236,13 +240,15 @@ def test_slots_past_the_pool_are_skipped_and_flagged():
 # ---------------------------------------------------------------- decode
 
 
-@pytest.mark.parametrize("G,B,D", [(1, 16, 128), (2, 8, 128), (4, 32, 128), (8, 64, 128), (8, 16, 64),
-                                   (4, 8, 64), (4, 128, 128), (2, 192, 128), (8, 256, 64), (1, 192, 64)])
-def test_decode_of_ragged_contexts(G, B, D):
+@pytest.mark.parametrize("G,B,D,path", [
+    (8, 16, 64, MMA), (4, 8, 64, MMA), (8, 256, 64, MMA), (1, 192, 64, MMA), (2, 32, 64, TC),
+    *[(G, B, 128, path) for path in (MMA, TC) for G, B in ((1, 16), (2, 8), (4, 32), (8, 64), (4, 128), (2, 192),
+                                                          (8, 256))]])
+def test_decode_of_ragged_contexts(G, B, D, path):
     ctxs = [1, 2, B - 1, B, B + 1, 3 * B + 2, 97, 128, 129, 700]
     wl = q4_workload("q4_ragged", G, B, 30 + G + B, ctxs, D=D)
     orc = OracleRun(wl)
-    cache, run = make(wl)
+    cache, run = make(wl, path=path)
     so, co, q, outs = orc.step(0)
     _, k, v = wl.step_values(0)
     sg, _, og = run.step(wl.decode_seqs, q, k, v)
@@ -252,13 +258,14 @@ def test_decode_of_ragged_contexts(G, B, D):
     assert cache.kv_pool_device_status() == 0
 
 
-@pytest.mark.parametrize("D,G,B", [(128, 4, 16), (64, 8, 16), (128, 8, 32), (128, 1, 8)])
-def test_fork_copy_on_write_and_the_planned_pass(D, G, B):
+@pytest.mark.parametrize("D,G,B,path", [(128, 4, 16, MMA), (64, 8, 16, MMA), (128, 8, 32, MMA), (128, 1, 8, MMA),
+                                        (128, 4, 16, TC), (128, 8, 32, TC), (128, 1, 8, TC), (128, 2, 192, TC)])
+def test_fork_copy_on_write_and_the_planned_pass(D, G, B, path):
     # two steps over two layers: the first copies the shared, partly filled
     # tail of the forks; the shared prefix is read once through the plan
     wl = q4_workload("q4_fork", G, B, 22, [1, 15, 17, 40, 300], fork=203, D=D, layers=2)
     orc = OracleRun(wl)
-    cache, run = make(wl)
+    cache, run = make(wl, path=path)
     assert same_pool(cache, orc.st)
     from paged_kv_cache_65_gb300.cache import parse_plan
     from paged_kv_cache_65_gb300.driver import to_device
@@ -275,7 +282,7 @@ def test_fork_copy_on_write_and_the_planned_pass(D, G, B):
             assert max_err(og.cpu().numpy()[ly], outs[ly]) <= tol
         h_plan, _, _ = run.plan(wl.decode_seqs, run.max_blocks(wl.decode_seqs))
         plan = parse_plan(h_plan)
-        assert plan["kernel"] == 2 and plan["n_shared_segs"] > 0
+        assert plan["kernel"] == path and (plan["n_shared_segs"] > 0 or B > 128)
         # the same step per sequence, in bfloat16
         d_table, d_lens, mb = run.tables(wl.decode_seqs)
         qd = to_device(q, "bf16", "cuda")
@@ -285,8 +292,9 @@ def test_fork_copy_on_write_and_the_planned_pass(D, G, B):
     assert cache.kv_pool_device_status() == 0
 
 
+@pytest.mark.parametrize("path", [MMA, TC])
 @pytest.mark.parametrize("n_br,G", [(3, 4), (4, 8), (8, 4), (5, 1)])
-def test_wide_shared_segments(n_br, G):
+def test_wide_shared_segments(n_br, G, path):
     # segments of 12 to 32 columns: two and four n-tiles
     B, H, D, prefix = 16, 2, 128, 1040
     n_blocks = prefix // B + 3 * n_br + 8
@@ -295,7 +303,7 @@ def test_wide_shared_segments(n_br, G):
     wl = synth.Workload("q4_wide", 1, n_blocks, B, H * G, H, D, "q4_0", 5,
                         synth.permutation((5, n_br), n_blocks), ops, list(range(n_br)))
     orc = OracleRun(wl)
-    cache, run = make(wl)
+    cache, run = make(wl, path=path)
     so, co, q, outs = orc.step(0)
     _, k, v = wl.step_values(0)
     sg, _, og = run.step(wl.decode_seqs, q, k, v, planned=True)
@@ -304,12 +312,13 @@ def test_wide_shared_segments(n_br, G):
     assert cache.kv_pool_device_status() == 0
 
 
+@pytest.mark.parametrize("path", [MMA, TC])
 @pytest.mark.parametrize("planned", [False, True])
-def test_unused_slots_of_nan_scales_do_not_leak(planned):
+def test_unused_slots_of_nan_scales_do_not_leak(planned, path):
     # every byte of the unused slots is 0xFF: codes of 7, scales with NaN bits
     wl = q4_workload("q4_nan", 4, 16, 23, [1, 15, 17, 70, 333], fork=150)
     orc = OracleRun(wl)
-    cache, run = make(wl, fill=0xFF)
+    cache, run = make(wl, fill=0xFF, path=path)
     so, co, q, outs = orc.step(0)
     _, k, v = wl.step_values(0)
     _, _, og = run.step(wl.decode_seqs, q, k, v, planned=planned)
@@ -319,10 +328,12 @@ def test_unused_slots_of_nan_scales_do_not_leak(planned):
     assert max_err(got, outs[0]) <= tol
 
 
-def test_empty_contexts_give_zeros_and_bad_tables_are_flagged():
+@pytest.mark.parametrize("path", [MMA, TC])
+def test_empty_contexts_give_zeros_and_bad_tables_are_flagged(path):
     from paged_kv_cache_65_gb300 import PagedKVCache, _lib
 
     c = PagedKVCache(1, 8, 16, 2, 128, "q4_0")
+    c.kv_pool_set_option(_lib.KV_OPT_DECODE_PATH, path)
     c.k.zero_()
     c.v.zero_()
     q = torch.ones((3, 8, 128), dtype=torch.bfloat16, device="cuda")
@@ -343,14 +354,16 @@ def test_empty_contexts_give_zeros_and_bad_tables_are_flagged():
     assert c.kv_pool_device_status() == _lib.KV_DEV_BAD_CONTEXT
 
 
+@pytest.mark.parametrize("path", [MMA, TC])
 @pytest.mark.parametrize("q_scale,k_scale,v_scale", [(1e-3, 1.0, 1.0), (30.0, 1.0, 1.0), (1.0, 1e-4, 1e-3),
                                                      (1e5, 1e-4, 1.0), (1e-6, 5e4, 4e4), (1.0, 8.0, 5e4)])
-def test_magnitudes_of_q_k_and_v(q_scale, k_scale, v_scale):
-    from paged_kv_cache_65_gb300 import PagedKVCache
+def test_magnitudes_of_q_k_and_v(q_scale, k_scale, v_scale, path):
+    from paged_kv_cache_65_gb300 import PagedKVCache, _lib
 
     rng = np.random.default_rng(41)
     n, B, H, G, D = 300, 16, 2, 4, 128
     c = PagedKVCache(1, 20, B, H, D, "q4_0")
+    c.kv_pool_set_option(_lib.KV_OPT_DECODE_PATH, path)
     st = KVStore(1, 20, B, H, D, "q4_0")
     xk = synth.storage_values((rng.standard_normal((n, H, D)) * k_scale).astype(np.float32), "q4_0")
     xv = synth.storage_values((rng.standard_normal((n, H, D)) * v_scale).astype(np.float32), "q4_0")
@@ -371,12 +384,14 @@ def test_magnitudes_of_q_k_and_v(q_scale, k_scale, v_scale):
     assert max_err(out.cpu().numpy()[0], ref) <= tol
 
 
-def test_long_context_and_offsets_past_32_bits():
+@pytest.mark.parametrize("path", [MMA, TC])
+def test_long_context_and_offsets_past_32_bits(path):
     # a pool whose byte offsets pass 2^32 and one sequence through its last blocks
-    from paged_kv_cache_65_gb300 import PagedKVCache
+    from paged_kv_cache_65_gb300 import PagedKVCache, _lib
 
     B, H, D, G, N = 32, 8, 128, 8, 260000  # N * H * B * 72 bytes = 4.8e9 of K
     c = PagedKVCache(1, N, B, H, D, "q4_0")
+    c.kv_pool_set_option(_lib.KV_OPT_DECODE_PATH, path)
     n = 5000
     rng = np.random.default_rng(2)
     nb = -(-n // B)
@@ -408,10 +423,11 @@ def test_long_context_and_offsets_past_32_bits():
     assert c.kv_pool_device_status() == 0
 
 
-def test_without_a_workspace_on_another_stream_and_in_a_graph():
+@pytest.mark.parametrize("path", [MMA, TC])
+def test_without_a_workspace_on_another_stream_and_in_a_graph(path):
     wl = q4_workload("q4_graph", 4, 16, 61, [5, 64, 333, 1000])
     orc = OracleRun(wl)
-    cache, run = make(wl)
+    cache, run = make(wl, path=path)
     so, co, q, outs = orc.step(0)
     _, k, v = wl.step_values(0)
     sg, _, og = run.step(wl.decode_seqs, q, k, v)

@@ -80,12 +80,13 @@ def test_device_tables_option(lib):
             c.kv_pool_set_option(lib.KV_OPT_DEVICE_TABLES, v)
 
 
-@pytest.mark.parametrize("path", [0, 2, 3])
-def test_plans_take_the_warp_level_pass(lib, path):
+@pytest.mark.parametrize("D,path,kernel", [(64, 0, 2), (64, 2, 2), (64, 3, 2), (128, 2, 2), (128, 3, 3)])
+def test_plans_follow_the_decode_path(lib, D, path, kernel):
     from paged_kv_cache_65_gb300 import PagedKVCache
     from paged_kv_cache_65_gb300.cache import parse_plan
 
-    c = PagedKVCache(1, 64, 16, 2, 128, "q4_0", allocate=False)
+    # the tcgen05 pass takes D_h = 128
+    c = PagedKVCache(1, 64, 16, 2, D, "q4_0", allocate=False)
     c.kv_pool_set_option(lib.KV_OPT_DECODE_PATH, path)
     c.seq_append_tokens(0, 512)
     for s in (1, 2, 3):
@@ -93,7 +94,7 @@ def test_plans_take_the_warp_level_pass(lib, path):
     c.seq_append_slots([1, 2, 3])
     buf, ws = c.paged_decode_plan([1, 2, 3], 16, 64)
     plan = parse_plan(buf)
-    assert plan["kernel"] == 2 and plan["n_shared_segs"] > 0 and ws > 0
+    assert plan["kernel"] == kernel and plan["n_shared_segs"] > 0 and ws > 0
 
 
 def test_oracle_store_round_trip():
