@@ -144,6 +144,29 @@ __device__ __forceinline__ void ldsm8_x2_t(uint32_t addr, uint32_t& r0, uint32_t
                : "r"(addr));
 }
 
+// mbar_wait_bounded for roles that wait most of their time: a failed try
+// suspends the warp for up to the hinted time (it resumes when the phase
+// completes) instead of polling, which takes issue slots from the warps that
+// work; the clock is read between tries only.
+__device__ __forceinline__ bool q4_try_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(100000u)  // ns
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool q4_wait(uint64_t* bar, uint32_t parity) {
+  if (q4_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (!q4_try_wait(bar, parity))
+    if (globaltimer_ns() - t0 > kWaitLimitNs) return false;
+  return true;
+}
+
 // Arrive `n` times.
 __device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
   asm volatile(
@@ -320,7 +343,7 @@ __global__ void __launch_bounds__(kQ4Threads, kQ4CtasPerSm) decode_q4_kernel(con
     auto publish = [&](const Piece& x, bool valid) {
       const int di = npub % kPieceRing;
       if (npub >= kPieceRing && alive) {
-        if (!mbar_wait_bounded(&dempty[di], ((npub / kPieceRing) - 1) & 1, kWaitLimitNs)) {
+        if (!q4_wait(&dempty[di], ((npub / kPieceRing) - 1) & 1)) {
           alive = false;
           if (lane == 0) record_status(a.status, 8);
         }
@@ -374,7 +397,7 @@ __global__ void __launch_bounds__(kQ4Threads, kQ4CtasPerSm) decode_q4_kernel(con
         const int slot = stage % NS;
         unsigned char* dst = st + slot * C::SLOT_BYTES + (lane & 15) * unit_bytes;
         if (stage >= NS && alive) {
-          if (!mbar_wait_bounded(&empty[slot], ((stage / NS) & 1) ^ 1, kWaitLimitNs)) {
+          if (!q4_wait(&empty[slot], ((stage / NS) & 1) ^ 1)) {
             alive = false;
             if (lane == 0) record_status(a.status, 8);
           }
@@ -404,7 +427,7 @@ __global__ void __launch_bounds__(kQ4Threads, kQ4CtasPerSm) decode_q4_kernel(con
     }
     const int first = stage > NS ? stage - NS : 0;
     for (int k = first; k < stage; ++k)
-      mbar_wait_bounded(&full[k % NS], (k / NS) & 1, kWaitLimitNs);
+      q4_wait(&full[k % NS], (k / NS) & 1);
     return;
   }
 
@@ -458,7 +481,7 @@ __global__ void __launch_bounds__(kQ4Threads, kQ4CtasPerSm) decode_q4_kernel(con
   int nread = 0;
   auto read_piece = [&](Piece& x) -> bool {
     const int di = nread % kPieceRing;
-    if (alive && !mbar_wait_bounded(&dfull[di], (nread / kPieceRing) & 1, kWaitLimitNs)) {
+    if (alive && !q4_wait(&dfull[di], (nread / kPieceRing) & 1)) {
       alive = false;
       if (lane == 0) record_status(a.status, 8);
     }
@@ -545,7 +568,7 @@ __global__ void __launch_bounds__(kQ4Threads, kQ4CtasPerSm) decode_q4_kernel(con
     const int n_slots = (p.tok_end - tok_first + C::TS - 1) / C::TS;
     for (int r = base + ((wt - base) & (WT - 1)); r < base + n_slots; r += WT) {
       const int slot = r % NS;
-      if (alive && !mbar_wait_bounded(&full[slot], (r / NS) & 1, kWaitLimitNs)) {
+      if (alive && !q4_wait(&full[slot], (r / NS) & 1)) {
         alive = false;
         if (lane == 0) record_status(a.status, 8);
       }

@@ -23,7 +23,7 @@ cudaError_t launch_decode_q4_tc(const DecodeArgs& a_in, int sm_count, int max_gr
     cudaFuncAttributes fa;
     e = cudaFuncGetAttributes(&fa, kern);
     if (e != cudaSuccess) return e;
-    if (fa.numRegs != 128) return cudaErrorInvalidConfiguration;
+    if (fa.numRegs != kQ4TcRegsLaunch) return cudaErrorInvalidConfiguration;
     attr_set[v][dev] = true;
   }
   if (*grid_io <= 0) *grid_io = sm_count < max_grid ? sm_count : max_grid;

@@ -30,11 +30,12 @@
 // exponents, is moved when a row's E passes it by more than 4, both with a
 // rescale of O^T; p is one rounding to 11 bits.
 //
-// Warps (one CTA of 16 per SM): 0-3 softmax (thread r owns token row r of a
-// stage and, at a piece's end, row r of O^T); 4-7 turn K rows into fp16 in
-// tensor memory, 8-11 V rows into fp16 in shared memory (M-major, 128-byte
-// swizzle); 12 copies the codes (a whole block of one head is one bulk copy),
-// 13 stages Q, 14 issues the S MMAs, 15 the P.V MMAs.  The codes' ring is
+// Warps (one CTA of 20 per SM): 0-3 and 4-7 softmax, each group half of the
+// columns (thread r owns token row r of a stage and, at a piece's end, row r of
+// O^T; a column's references are its group's own, so the groups never meet);
+// 8-11 turn K rows into fp16 in tensor memory, 12-15 V rows into fp16 in shared
+// memory (M-major, 128-byte swizzle); 16 copies the codes (a whole block of one
+// head is one bulk copy), 17 stages Q, 18 issues the S MMAs, 19 the P.V MMAs.  The codes' ring is
 // free again as soon as they are converted, so its five stages (92 KB) are
 // all in flight while the converted stages (three of K, two of V and P) are
 // worked on.
@@ -55,11 +56,12 @@ struct Q4Tc {
   static constexpr int CODES = TS * ROW;        // K (or V) codes of a stage
   static constexpr int NC = 5;                  // stages of codes in the ring
   static constexpr int NK = 3;                  // converted K stages (tensor memory)
-  static constexpr int NV = 2;                  // converted V stages, and P
-  static constexpr int NKP = 8;                 // K rows' powers: the converters may be NK + 2 ahead
+  static constexpr int NV = 2;                  // converted V stages (shared memory)
+  static constexpr int NP = 4;                  // stages of weights
+  static constexpr int NKP = 8;                 // rows' powers: the converters may be NK + 2 ahead
   static constexpr int HALF = TS * 128;         // 64 dimensions of a converted V stage
   static constexpr int VBUF = 2 * HALF;
-  static constexpr int PBUF = TS * 128;
+  static constexpr int PBUF = TS * 64;          // 32 columns a token
   static constexpr int QHALF = 32 * 128;
   static constexpr int QTILE = 2 * QHALF;
   static constexpr int QBUF = 2;
@@ -69,22 +71,24 @@ struct Q4Tc {
   static constexpr int TM_COLS = 512;
   static constexpr float TAU = 8.f;             // base-2 headroom of the scores' reference
   static constexpr int ETAU = 4;                // and of V's exponents
-  static constexpr int WARPS = 16;
-  static constexpr int NBARS = 2 * NC + 2 * NK + 2 * NV + 4 + NV + 2 * QBUF + 2;
+  static constexpr int WARPS = 20;
+  static constexpr int NBARS = 2 * NC + 2 * NK + NV + 4 + 2 * NP + 2 * QBUF + 2;
 };
 static_assert(Q4Tc::TM_K + Q4Tc::NK * 64 <= Q4Tc::TM_COLS, "TMEM columns");
 constexpr int kQ4TcThreads = Q4Tc::WARPS * 32;
-// registers a thread per warpgroup (softmax, K and V converters, helpers)
-// against the 128 that 16 warps are launched with
-constexpr int kQ4TcRegsSoftmax = 208, kQ4TcRegsCvt = 112, kQ4TcRegsHelper = 80;
-static_assert(kQ4TcRegsSoftmax + 2 * kQ4TcRegsCvt + kQ4TcRegsHelper <= 4 * 128, "register split");
+// registers a thread per warpgroup (two softmax, K and V converters, helpers)
+// against the 96 that 20 warps are launched with (the launcher checks it)
+constexpr int kQ4TcRegsLaunch = 96;
+constexpr int kQ4TcRegsSoftmax = 120, kQ4TcRegsCvt = 96, kQ4TcRegsHelper = 48;
+static_assert(2 * kQ4TcRegsSoftmax + 2 * kQ4TcRegsCvt + kQ4TcRegsHelper <= 5 * kQ4TcRegsLaunch,
+              "register split");
 
 constexpr int decode_q4_tc_smem_bytes() {
   using C = Q4Tc;
-  return C::NV * (C::VBUF + C::PBUF) + C::QBUF * C::QTILE  // 1 KiB aligned operands
+  return C::NV * C::VBUF + C::NP * C::PBUF + C::QBUF * C::QTILE  // 1 KiB aligned operands
          + 2 * C::NC * C::CODES                            // codes
-         + (C::NKP + C::NV) * C::TS * 4                    // rows' powers of two: K, V
-         + 4 * 4 * 32 * 4                                  // column maxima, sums, factors
+         + 2 * C::NKP * C::TS * 4                            // rows' powers of two: K, V
+         + 2 * 4 * 128 * 4                                 // per softmax group: maxima, sums
          + 64                                              // Q factors, exponent maxima
          + C::NBARS * 8 + 4 * 8 + 16                       // mbarriers, walk state, TMEM address
          + kTableCache * 4 + 128                           // table cache, start record
@@ -101,6 +105,20 @@ __device__ __forceinline__ float q4_pow2(int e) {
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
+__device__ __forceinline__ float q4_max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// E of a row with these scales (fp16 bits): floor(log2) of the largest, -24 for
+// zeros.
+__device__ __forceinline__ int q4_row_exp(const uint32_t (&sc)[2]) {
+  const float mx = fmaxf(fmaxf(half_lo(sc[0]), half_hi(sc[0])), fmaxf(half_lo(sc[1]), half_hi(sc[1])));
+  const int E = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
+  return E < -24 ? -24 : E;
+}
+
 // Multipliers of one token row from its four scales (fp16 bits): E, and per
 // pair of groups A = d 2^(14-E).  live = false: all zero, so that whatever the
 // row holds becomes zeros.
@@ -111,10 +129,7 @@ __device__ __forceinline__ int q4_row_scales(const uint32_t (&sc)[2], bool live,
     d[2 * i] = half_lo(sc[i]);
     d[2 * i + 1] = half_hi(sc[i]);
   }
-  const float mx = fmaxf(fmaxf(d[0], d[1]), fmaxf(d[2], d[3]));
-  // 0 and subnormal scales take fp16's smallest exponents; zero rows -24
-  int E = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
-  E = E < -24 ? -24 : E;
+  const int E = q4_row_exp(sc);
   const float f = live ? q4_pow2(14 - E) : 0.f;
 #pragma unroll
   for (int i = 0; i < 2; ++i)
@@ -122,8 +137,8 @@ __device__ __forceinline__ int q4_row_scales(const uint32_t (&sc)[2], bool live,
   return E;
 }
 
-// Sixteen nibbles' words of one group (16 bytes) to 32 fp16 values.
-__device__ __forceinline__ void q4_convert(const uint32_t (&w)[4], __half2 a_lo, uint32_t (&h)[16]) {
+// The words of one group (16 bytes) to 32 fp16 values.
+__device__ __forceinline__ void q4_convert(const uint32_t (&w)[4], __half2 a_lo, uint32_t* h) {
   const __half2 a_hi = __hmul2(a_lo, __half2(__ushort_as_half(0x2c00), __ushort_as_half(0x2c00)));   // 2^-4
   const __half2 b = __hmul2(a_lo, __half2(__ushort_as_half(0x8008), __ushort_as_half(0x8008)));      // -2^-21
   auto cv = [&](uint32_t x, __half2 m) -> uint32_t {
@@ -140,36 +155,72 @@ __device__ __forceinline__ void q4_convert(const uint32_t (&w)[4], __half2 a_lo,
   }
 }
 
+// 16 columns of tensor memory, without the wait for it
+__device__ __forceinline__ void tmem_st16_nowait(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
 // State of the softmax warps for one CTA.
 struct Q4TcSoftmax {
   const DecodeArgs* a;
   unsigned char* p_st;
   const float* k_pow;   // [NKP][128] 2^(E + 10) of the K rows
-  const float* v_exp;   // [NV][128] E of the V rows
+  const float* v_exp;   // [NKP][128] E of the V rows
   const float* q_fac;   // [QBUF] score factor of the piece
   float *red, *cmx, *lsum;
   float* emx;           // [4] exponent maxima per warp
-  uint64_t *s_full, *s_empty, *v_full, *p_full, *pv_done, *o_free, *q_full, *q_empty;
+  uint64_t *s_full, *s_empty, *p_full, *pv_done, *o_free, *q_full, *q_empty;
   uint32_t tmem;
   int cstride;
+  int grp;              // softmax group: warps 4 grp .. 4 grp + 3
   bool alive;
   int stage, npiece;
 
-  __device__ bool wait(uint64_t* bar, uint32_t parity) {
-    if (alive && !mbar_wait_bounded(bar, parity, kWaitLimitNs)) {
-      alive = false;
+  // Lane 0 of the warp waits, the others follow it: fewer polls in the way of
+  // the warps that work.
+  __device__ void wait(uint64_t* bar, uint32_t parity) {
+    bool ok = alive;
+    if (ok && (threadIdx.x & 31) == 0 && !q4_wait(bar, parity)) {
+      ok = false;
       record_status(a->status, 8);
     }
-    return alive;
+    alive = __all_sync(0xffffffffu, ok);
   }
 
-  template <int NCP>
-  __device__ void run(const Piece& p, int n_st, int tok_first) {
+  // A piece without columns for this group: it keeps its place in the stages.
+  __device__ void idle(int n_st) {
     using C = Q4Tc;
-    const int t = threadIdx.x;  // token row of a stage / row of O^T
+    const bool first = (threadIdx.x & 31) == 0;
+    wait(&q_full[npiece % C::QBUF], (npiece / C::QBUF) & 1);
+    if (first) mbar_arrive(&q_empty[npiece % C::QBUF]);
+    for (int i = 0; i < n_st; ++i, ++stage) {
+      wait(&s_full[stage & 1], (stage >> 1) & 1);
+      if (first) {
+        mbar_arrive(&s_empty[stage & 1]);
+        mbar_arrive(&p_full[stage % C::NP]);
+      }
+    }
+    // O^T is given back only after the piece's last MMAs, so that this group
+    // never stands in for the other one at a later piece
+    wait(&pv_done[(stage - 1) % C::NP], ((stage - 1) / C::NP) & 1);
+    if (first) mbar_arrive(o_free);
+    ++npiece;
+  }
+
+  // Columns c_first .. c_first + NCP - 1 of one piece.
+  template <int NCP>
+  __device__ void run(const Piece& p, int n_st, int tok_first, int c_first) {
+    using C = Q4Tc;
+    const int t = threadIdx.x & 127;  // token row of a stage / row of O^T
     const int warp = t >> 5, lane = t & 31;
-    const uint32_t tl = static_cast<uint32_t>(warp * 32) << 16;
-    const int ncols = p.ncols;
+    const int bar = 1 + grp;
+    const uint32_t tl = (static_cast<uint32_t>(warp * 32) << 16) + c_first;
+    const int ncols = min(p.ncols - c_first, NCP);
     float m_ref[NCP], l_part[NCP];
 #pragma unroll
     for (int c = 0; c < NCP; ++c) {
@@ -186,24 +237,21 @@ struct Q4TcSoftmax {
       const int nvalid = min(p.tok_end - (tok_first + i * C::TS), C::TS);
       const bool valid = t < nvalid;
       wait(&s_full[stage & 1], (stage >> 1) & 1);
-      wait(&v_full[stage % C::NV], (stage / C::NV) & 1);  // its rows' exponents
       __syncwarp();
       tc_fence_after();
       uint32_t sr[NCP];
       tmem_ld<NCP>(tmem + C::TM_S + (stage & 1) * 32 + tl, sr);
       const float kf = qs * k_pow[(stage % C::NKP) * C::TS + t];
-      const float ve = v_exp[(stage % C::NV) * C::TS + t];
+      const float ve = v_exp[(stage % C::NKP) * C::TS + t];
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&s_empty[stage & 1]);
-      float x[NCP];
-      bool exceed = ve > e_ref + C::ETAU;
+      float x[NCP], top = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < NCP; ++c) {
-        x[c] = fmaf(__uint_as_float(sr[c]), kf, -m_ref[c]);
-        exceed |= x[c] > C::TAU;
-      }
-      if (bar_or_sync(1, 128, valid && exceed)) {
+      for (int c = 0; c < NCP; ++c) x[c] = fmaf(__uint_as_float(sr[c]), kf, -m_ref[c]);
+#pragma unroll
+      for (int c = 0; c < NCP; c += 2) top = q4_max3(top, x[c], x[c + 1]);
+      if (bar_or_sync(bar, 128, valid && (top > C::TAU || ve > e_ref + C::ETAU))) {
         // ---- a reference moves: exact column maxima (and the largest V
         // exponent) of this stage
         float v[NCP];
@@ -215,7 +263,7 @@ struct Q4TcSoftmax {
 #pragma unroll
         for (int off = 16; off; off >>= 1) em = fmaxf(em, __shfl_xor_sync(0xffffffffu, em, off));
         if (lane == 0) emx[warp] = em;
-        named_bar_sync(1, 128);
+        named_bar_sync(bar, 128);
         float cm = -INFINITY;
         if (lane < NCP) {
 #pragma unroll
@@ -237,7 +285,7 @@ struct Q4TcSoftmax {
         }
         if (i > 0) {
           // rescale O^T once the previous stage's MMAs are done with it
-          wait(&pv_done[(stage - 1) % C::NV], ((stage - 1) / C::NV) & 1);
+          wait(&pv_done[(stage - 1) % C::NP], ((stage - 1) / C::NP) & 1);
           __syncwarp();
           tc_fence_after();
           uint32_t o[NCP];
@@ -248,12 +296,13 @@ struct Q4TcSoftmax {
           tmem_st<NCP>(tmem + C::TM_O + tl, o);
         }
       }
-      // ---- weights: row t of P' (N-major, 128-byte swizzle), into the buffer
-      // that the MMAs of two stages before have read
-      if (stage >= C::NV) wait(&pv_done[stage % C::NV], ((stage / C::NV) - 1) & 1);
+      // ---- weights: row t of P' (N-major, 64-byte swizzle: 16-byte chunk c at
+      // c ^ (t / 2 mod 4)), into the buffer that the MMAs of four stages before
+      // have read
+      if (stage >= C::NP) wait(&pv_done[stage % C::NP], ((stage / C::NP) - 1) & 1);
       // a power of two; 0 for a row past the context, whose exponent may be any
       const __half2 pe = __float2half2_rn(valid ? exp2_approx(ve - e_ref) : 0.f);
-      const uint32_t pb = smem_u32(p_st + (stage % C::NV) * C::PBUF) + t * 128;
+      const uint32_t pb = smem_u32(p_st + (stage % C::NP) * C::PBUF) + t * 64;
 #pragma unroll
       for (int c8 = 0; c8 < NCP / 8; ++c8) {
         uint32_t hi[4];
@@ -267,22 +316,22 @@ struct Q4TcSoftmax {
           const __half2 ph = __hmul2(__floats2half2_rn(p0, p1), pe);
           hi[k] = *reinterpret_cast<const uint32_t*>(&ph);
         }
-        sts128(pb + ((c8 ^ (t & 7)) << 4), hi[0], hi[1], hi[2], hi[3]);
+        sts128(pb + (((c_first / 8 + c8) ^ ((t >> 1) & 3)) << 4), hi[0], hi[1], hi[2], hi[3]);
       }
       fence_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[stage % C::NV]);
+      if (lane == 0) mbar_arrive(&p_full[stage % C::NP]);
     }
 
     // ---- end of the piece: O^T from TMEM once the last stage's MMAs are
     // done, l reduced over the 128 rows
-    wait(&pv_done[(stage - 1) % C::NV], ((stage - 1) / C::NV) & 1);
+    wait(&pv_done[(stage - 1) % C::NP], ((stage - 1) / C::NP) & 1);
     __syncwarp();
     tc_fence_after();
     const long long slot_id = (long long)blockIdx.x + p.seg;
     const float of = exp2_approx(e_ref + 10.f);
-    float* dst = a->ws_o + slot_id * cstride * C::D + q4_dim(t);
+    float* dst = a->ws_o + (slot_id * cstride + c_first) * C::D + q4_dim(t);
 #pragma unroll
     for (int c0 = 0; c0 < NCP; c0 += 8) {
       uint32_t o[8];
@@ -296,7 +345,7 @@ struct Q4TcSoftmax {
     if (lane == 0) mbar_arrive(o_free);
     const float ls = warp_column_reduce<NCP, false>(l_part);
     if (lane < NCP) lsum[warp * 32 + lane] = ls;
-    named_bar_sync(1, 128);
+    named_bar_sync(bar, 128);
     if (warp == 0 && lane < ncols) {
       float mc = m_ref[0];
 #pragma unroll
@@ -304,8 +353,8 @@ struct Q4TcSoftmax {
       float L = 0.f;
 #pragma unroll
       for (int w = 0; w < 4; ++w) L += lsum[w * 32 + lane];
-      a->ws_ml[(slot_id * cstride + lane) * 2] = mc;
-      a->ws_ml[(slot_id * cstride + lane) * 2 + 1] = L;
+      a->ws_ml[(slot_id * cstride + c_first + lane) * 2] = mc;
+      a->ws_ml[(slot_id * cstride + c_first + lane) * 2 + 1] = L;
     }
     ++npiece;
   }
@@ -319,26 +368,26 @@ __global__ void __launch_bounds__(kQ4TcThreads, 1) decode_q4_tc_kernel(const Dec
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   unsigned char* v_st = smem;
   unsigned char* p_st = v_st + C::NV * C::VBUF;
-  unsigned char* q_s = p_st + C::NV * C::PBUF;
+  unsigned char* q_s = p_st + C::NP * C::PBUF;
   unsigned char* k_code = q_s + C::QBUF * C::QTILE;
   unsigned char* v_code = k_code + C::NC * C::CODES;
   float* k_pow = reinterpret_cast<float*>(v_code + C::NC * C::CODES);
   float* v_exp = k_pow + C::NKP * C::TS;
-  float* red = v_exp + C::NV * C::TS;
-  float* cmx = red + 128;
-  float* lsum = cmx + 128;
-  float* q_fac = lsum + 2 * 128;  // [QBUF]
-  float* emx = q_fac + 8;         // [4]
+  float* red = v_exp + C::NKP * C::TS;
+  float* cmx = red + 2 * 128;  // these three [group][4][32]
+  float* lsum = cmx + 2 * 128;
+  float* q_fac = lsum + 4 * 128;  // [QBUF]
+  float* emx = q_fac + 8;         // [group][4]
   uint64_t* full = reinterpret_cast<uint64_t*>(emx + 8);  // [NC] codes in
   uint64_t* empty = full + C::NC;                         // [NC] codes converted
   uint64_t* k_full = empty + C::NC;                       // [NK] K rows in TMEM
   uint64_t* k_empty = k_full + C::NK;                     // [NK] S MMAs done
   uint64_t* v_full = k_empty + C::NK;                     // [NV] V rows converted
-  uint64_t* pv_done = v_full + C::NV;                     // [NV] P.V MMAs done
-  uint64_t* s_full = pv_done + C::NV;                     // [2]
+  uint64_t* pv_done = v_full + C::NV;                     // [NP] P.V MMAs done
+  uint64_t* s_full = pv_done + C::NP;                     // [2]
   uint64_t* s_empty = s_full + 2;                         // [2]
-  uint64_t* p_full = s_empty + 2;                         // [NV]
-  uint64_t* q_full = p_full + C::NV;                      // [QBUF]
+  uint64_t* p_full = s_empty + 2;                         // [NP]
+  uint64_t* q_full = p_full + C::NP;                      // [QBUF]
   uint64_t* q_empty = q_full + C::QBUF;                   // [QBUF]
   uint64_t* o_free = q_empty + C::QBUF;
   uint64_t* fin = o_free + 1;
@@ -371,20 +420,20 @@ __global__ void __launch_bounds__(kQ4TcThreads, 1) decode_q4_tc_kernel(const Dec
       mbar_init(&k_full[i], 4);
       mbar_init(&k_empty[i], 1);
     }
-    for (int i = 0; i < C::NV; ++i) {
-      mbar_init(&v_full[i], 4);
+    for (int i = 0; i < C::NV; ++i) mbar_init(&v_full[i], 4);
+    for (int i = 0; i < C::NP; ++i) {
       mbar_init(&pv_done[i], 1);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&p_full[i], 8);  // softmax warps
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], 4);
+      mbar_init(&s_empty[i], 8);
     }
     for (int i = 0; i < C::QBUF; ++i) {
       mbar_init(&q_full[i], 1);
-      mbar_init(&q_empty[i], 5);  // the S MMAs done, the factor read by four warps
+      mbar_init(&q_empty[i], 9);  // the S MMAs done, the factor read by eight warps
     }
-    mbar_init(o_free, 4);
+    mbar_init(o_free, 8);
     mbar_init(fin, 2);
     fence_barrier_init();
   }
@@ -396,7 +445,7 @@ __global__ void __launch_bounds__(kQ4TcThreads, 1) decode_q4_tc_kernel(const Dec
   // them (decode_q4.cuh)
   if (a.meta_wait) griddep_wait();
   const bool use_rec = PLAN && a.starts != nullptr && a.start_grid == a.grid;
-  if (warp == 12) {
+  if (warp == 16) {
     if constexpr (PLAN) {
       const long long W = a.plan_W;
       long long chunk = (W + a.grid - 1) / a.grid;
@@ -495,7 +544,7 @@ __global__ void __launch_bounds__(kQ4TcThreads, 1) decode_q4_tc_kernel(const Dec
     griddep_wait();
     griddep_launch_dependents();
     if constexpr (!PLAN) {
-      if (blockIdx.x == 0 && warp == 12)
+      if (blockIdx.x == 0 && warp == 16)
         write_prefix(a.ctx, a.n_seq, B, H, a.max_blocks, a.ws_pre);
     }
   };
@@ -504,15 +553,17 @@ __global__ void __launch_bounds__(kQ4TcThreads, 1) decode_q4_tc_kernel(const Dec
     return n > 0 ? (n + C::TS - 1) / C::TS : 0;
   };
   bool alive = true;
-  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    if (alive && !mbar_wait_bounded(bar, parity, kWaitLimitNs)) {
-      alive = false;
+  // whole warps: lane 0 waits, the others follow it
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    bool ok = alive;
+    if (ok && lane == 0 && !q4_wait(bar, parity)) {
+      ok = false;
       record_status(a.status, 8);
     }
-    return alive;
+    alive = __all_sync(0xffffffffu, ok);
   };
 
-  if (warp < 4) {
+  if (warp < 8) {
     // ------------------------------------------------------ softmax warps
     reg_alloc<kQ4TcRegsSoftmax>();
     wait_previous_grid();
@@ -522,13 +573,13 @@ __global__ void __launch_bounds__(kQ4TcThreads, 1) decode_q4_tc_kernel(const Dec
     sm.k_pow = k_pow;
     sm.v_exp = v_exp;
     sm.q_fac = q_fac;
-    sm.red = red;
-    sm.cmx = cmx;
-    sm.lsum = lsum;
-    sm.emx = emx;
+    sm.grp = warp >> 2;
+    sm.red = red + sm.grp * 128;
+    sm.cmx = cmx + sm.grp * 128;
+    sm.lsum = lsum + sm.grp * 128;
+    sm.emx = emx + sm.grp * 4;
     sm.s_full = s_full;
     sm.s_empty = s_empty;
-    sm.v_full = v_full;
     sm.p_full = p_full;
     sm.pv_done = pv_done;
     sm.o_free = o_free;
@@ -545,109 +596,116 @@ __global__ void __launch_bounds__(kQ4TcThreads, 1) decode_q4_tc_kernel(const Dec
       if (n_st == 0) {
         // no block of this piece: an empty partial that the merge skips
         const long long slot_id = (long long)blockIdx.x + p.seg;
-        for (int c = 0; c < p.ncols; ++c)
-          a.ws_o[(slot_id * sm.cstride + c) * C::D + threadIdx.x] = 0.f;
-        if (threadIdx.x < p.ncols) {
-          a.ws_ml[(slot_id * sm.cstride + threadIdx.x) * 2] = -INFINITY;
-          a.ws_ml[(slot_id * sm.cstride + threadIdx.x) * 2 + 1] = 0.f;
+        if (sm.grp == 0) {
+          for (int c = 0; c < p.ncols; ++c)
+            a.ws_o[(slot_id * sm.cstride + c) * C::D + threadIdx.x] = 0.f;
+          if (threadIdx.x < p.ncols) {
+            a.ws_ml[(slot_id * sm.cstride + threadIdx.x) * 2] = -INFINITY;
+            a.ws_ml[(slot_id * sm.cstride + threadIdx.x) * 2 + 1] = 0.f;
+          }
         }
         continue;
       }
-      if (p.ncols <= 8)
-        sm.template run<8>(p, n_st, p.b0 * B);
-      else if (p.ncols <= 16)
-        sm.template run<16>(p, n_st, p.b0 * B);
+      // the columns in two halves; up to eight are one group's
+      const int half = p.ncols <= 16 ? 8 : 16, c_first = sm.grp * half;
+      if (c_first >= p.ncols)
+        sm.idle(n_st);
+      else if (half == 8)
+        sm.template run<8>(p, n_st, p.b0 * B, c_first);
       else
-        sm.template run<32>(p, n_st, p.b0 * B);
+        sm.template run<16>(p, n_st, p.b0 * B, c_first);
     }
-  } else if (warp < 12) {
-    // -------------------------------------------- converters (K 4-7, V 8-11)
-    reg_dealloc<kQ4TcRegsCvt>();
+  } else if (warp < 16) {
+    // ------------------------------------------ converters (K 8-11, V 12-15)
     wait_previous_grid();
-    const bool kp = warp < 8;
-    const int r = (threadIdx.x - 128) & 127;  // token row of a stage
+    const bool kp = warp < 12;
+    const int r = threadIdx.x & 127;  // token row of a stage
     const uint32_t tl = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const int ro = r & (UR - 1);
     const uint32_t unit = (r >> lur) * unit_bytes;
-    const uint32_t code_off = unit + ro * 16;
-    const uint32_t sc_off = unit + UR * 64 + (kp ? ro * 8 : ro * 2);
-    int stage = 0;
+    const uint32_t code_off = smem_u32(kp ? k_code : v_code) + unit + ro * 16;
+    const uint32_t ks_off = smem_u32(k_code) + unit + UR * 64 + ro * 8;
+    const uint32_t vs_off = smem_u32(v_code) + unit + UR * 64 + ro * 2;
+    // 16-byte chunk ch of a converted V row at ch ^ (r mod 8) in its half
+    const uint32_t v_row = smem_u32(v_st) + r * 128 + ((r & 7) << 4);
+    int stage = 0, slot = 0;
+    uint32_t slot_par = 0;
     Piece p;
     while (next_piece(p)) {
-      const int n_st = stages_of(p);
-      for (int i = 0; i < n_st; ++i, ++stage) {
-        const int slot = stage % C::NC;
-        wait(&full[slot], (stage / C::NC) & 1);
-        if (kp) {
-          if (stage >= C::NK) wait(&k_empty[stage % C::NK], ((stage / C::NK) - 1) & 1);
-        } else {
-          if (stage >= C::NV) wait(&pv_done[stage % C::NV], ((stage / C::NV) - 1) & 1);
-        }
-        alive = __all_sync(0xffffffffu, alive);
-        if (!alive) continue;
-        const bool live = r < p.tok_end - (p.b0 * B + i * C::TS);
-        const uint32_t base = smem_u32((kp ? k_code : v_code) + slot * C::CODES);
-        uint32_t sc[2];
-        if (kp) {
-          lds_scales<4>(base + sc_off, sc);
-        } else {
+      for (int left = p.tok_end - p.b0 * B; left > 0; left -= C::TS, ++stage) {
+        wait(&full[slot], slot_par);
+        const uint32_t sb = slot * C::CODES;
+        const bool live = r < left;
+        // V's scales of the row (both kinds of warps: the K warps, which run
+        // ahead, publish the exponents the softmax needs)
+        uint32_t vsc[2];
+        {
           uint16_t s4[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(s4[q]) : "r"(base + sc_off + q * UR * 2));
-          sc[0] = s4[0] | (static_cast<uint32_t>(s4[1]) << 16);
-          sc[1] = s4[2] | (static_cast<uint32_t>(s4[3]) << 16);
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(s4[q]) : "r"(vs_off + sb + q * UR * 2));
+          vsc[0] = s4[0] | (static_cast<uint32_t>(s4[1]) << 16);
+          vsc[1] = s4[2] | (static_cast<uint32_t>(s4[3]) << 16);
         }
-        uint32_t w[4][4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          lds128(base + code_off + q * UR * 16, w[q][0], w[q][1], w[q][2], w[q][3]);
         __half2 A[2];
-        const int E = q4_row_scales(sc, live, A);
-        // the codes are in registers: their stage may be copied over
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[slot]);
         if (kp) {
-          tc_fence_after();
-          const uint32_t tcol = tmem + tl + C::TM_K + (stage % C::NK) * 64;
+          uint32_t ksc[2];
+          lds_scales<4>(ks_off + sb, ksc);
+          k_pow[(stage % C::NKP) * C::TS + r] = q4_pow2(q4_row_scales(ksc, live, A) + 10);
+          v_exp[(stage % C::NKP) * C::TS + r] = static_cast<float>(q4_row_exp(vsc));
+          if (stage >= C::NK) wait(&k_empty[stage % C::NK], ((stage / C::NK) - 1) & 1);
+        } else {
+          q4_row_scales(vsc, live, A);
+          if (stage >= C::NV)
+            wait(&pv_done[(stage - C::NV) % C::NP], ((stage - C::NV) / C::NP) & 1);
+        }
+        if (!alive) continue;
+        tc_fence_after();
+        // one group at a time, the loop not unrolled: five kinds of warps share
+        // an SM sub-partition's instruction fetch, and short loops stay in it
+        const uint32_t out = kp ? tmem + tl + C::TM_K + (stage % C::NK) * 64
+                                : v_row + (stage % C::NV) * C::VBUF;
+        uint32_t a01 = *reinterpret_cast<const uint32_t*>(&A[0]);
+        uint32_t a23 = *reinterpret_cast<const uint32_t*>(&A[1]);
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          uint32_t w[4], h[16];
+          lds128(code_off + sb + q * UR * 16, w[0], w[1], w[2], w[3]);
+          const uint32_t aa = __byte_perm(a01, a01, 0x1010);
+          a01 = __byte_perm(a01, a23, 0x5432);  // the next group's scale
+          a23 >>= 16;
+          q4_convert(w, *reinterpret_cast<const __half2*>(&aa), h);
+          if (kp) {
+            tmem_st16_nowait(out + q * 16, h);
+          } else {
+            // chunks 4 q .. 4 q + 3 of the row: half q / 2
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            uint32_t h[2][16];
-            q4_convert(w[2 * hf], __low2half2(A[hf]), h[0]);
-            q4_convert(w[2 * hf + 1], __high2half2(A[hf]), h[1]);
-            uint32_t x[32];
-#pragma unroll
-            for (int k = 0; k < 32; ++k) x[k] = h[k >> 4][k & 15];
-            tmem_st32_nowait(tcol + hf * 32, x);
+            for (int k = 0; k < 4; ++k)
+              sts128((out + (q >> 1) * C::HALF) ^ ((4 * (q & 1) + k) << 4), h[4 * k], h[4 * k + 1],
+                     h[4 * k + 2], h[4 * k + 3]);
           }
-          k_pow[(stage % C::NKP) * C::TS + r] = q4_pow2(E + 10);
+        }
+        // the codes have been read: their stage may be copied over
+        if (kp) {
           tmem_wait_st();
           tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&k_full[stage % C::NK]);
         } else {
-          const uint32_t row = smem_u32(v_st + (stage % C::NV) * C::VBUF) + r * 128;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t h[16];
-            q4_convert(w[q], q & 1 ? __high2half2(A[q >> 1]) : __low2half2(A[q >> 1]), h);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int ch = 4 * q + k;  // 16-byte chunk of the row: dimensions 8 ch ..
-              sts128(row + (ch >> 3) * C::HALF + (((ch & 7) ^ (r & 7)) << 4), h[4 * k],
-                     h[4 * k + 1], h[4 * k + 2], h[4 * k + 3]);
-            }
-          }
-          v_exp[(stage % C::NV) * C::TS + r] = static_cast<float>(E);
           fence_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&v_full[stage % C::NV]);
+        }
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&empty[slot]);
+          mbar_arrive(kp ? &k_full[stage % C::NK] : &v_full[stage % C::NV]);
+        }
+        if (++slot == C::NC) {
+          slot = 0;
+          slot_par ^= 1;
         }
       }
     }
   } else {
     reg_dealloc<kQ4TcRegsHelper>();
-    if (warp == 12) {
+    if (warp == 16) {
       // --------------------------------------------------------- code copies
       TableCache tc;
       tc.ent = tcache;
@@ -688,7 +746,6 @@ __global__ void __launch_bounds__(kQ4TcThreads, 1) decode_q4_tc_kernel(const Dec
           const int slot = stage % C::NC;
           unsigned char* dst = st + slot * C::CODES + (lane & 15) * unit_bytes;
           if (stage >= C::NC) wait(&empty[slot], ((stage / C::NC) & 1) ^ 1);
-          alive = __all_sync(0xffffffffu, alive);
           if (!alive) continue;
           if (lane == 0) mbar_arrive_expect_tx(&full[slot], 2u * n_units * unit_bytes);
           __syncwarp();
@@ -710,8 +767,8 @@ __global__ void __launch_bounds__(kQ4TcThreads, 1) decode_q4_tc_kernel(const Dec
       // copies still in flight land before the CTA may exit
       const int first = stage > C::NC ? stage - C::NC : 0;
       for (int k = first; k < stage && alive; ++k)
-        alive = mbar_wait_bounded(&full[k % C::NC], (k / C::NC) & 1, kWaitLimitNs);
-    } else if (warp == 13) {
+        alive = q4_wait(&full[k % C::NC], (k / C::NC) & 1);
+    } else if (warp == 17) {
       // ------------------------------------------------------------ Q tiles
       wait_previous_grid();
       int np = 0;
@@ -720,7 +777,6 @@ __global__ void __launch_bounds__(kQ4TcThreads, 1) decode_q4_tc_kernel(const Dec
         if (stages_of(p) == 0) continue;
         const int qb = np % C::QBUF;
         if (np >= C::QBUF) wait(&q_empty[qb], ((np / C::QBUF) - 1) & 1);
-        alive = __all_sync(0xffffffffu, alive);
         // 16-byte chunk (column, eight dimensions) k * 32 + lane: two columns
         // a step, the columns past the piece's zero
         const int cols = p.ncols <= 16 ? 16 : 32;  // N of its S MMAs
@@ -776,68 +832,79 @@ __global__ void __launch_bounds__(kQ4TcThreads, 1) decode_q4_tc_kernel(const Dec
         ++np;
       }
     } else {
-      // ----------------------------------- MMA issuers: 14 for S, 15 for P.V
+      // ----------------------------------- MMA issuers: 18 for S, 19 for P.V.
+      // The whole warp walks and waits, so that descriptors are the warp's
+      // (uniform) values, and one lane issues.
       wait_previous_grid();
-      if (lane == 0) {
-        int stage = 0, np = 0;
-        Piece p;
-        if (warp == 14) {
-          constexpr uint32_t idS16 = idesc_f16(128, 16, false, false);
-          constexpr uint32_t idS32 = idesc_f16(128, 32, false, false);
-          while (next_piece(p)) {
-            const int n_st = stages_of(p);
-            if (n_st == 0) continue;
-            const uint32_t id = p.ncols <= 16 ? idS16 : idS32;
-            const int qb = np % C::QBUF;
-            const uint32_t qbase = smem_u32(q_s + qb * C::QTILE);
-            wait(&q_full[qb], (np / C::QBUF) & 1);
-            for (int i = 0; i < n_st; ++i, ++stage) {
-              if (stage >= 2) wait(&s_empty[stage & 1], ((stage >> 1) - 1) & 1);
-              wait(&k_full[stage % C::NK], (stage / C::NK) & 1);
-              if (!alive) continue;
-              tc_fence_after();
+      const bool one = lane == 0;
+      int stage = 0, np = 0;
+      Piece p;
+      if (warp == 18) {
+        constexpr uint32_t idS16 = idesc_f16(128, 16, false, false);
+        constexpr uint32_t idS32 = idesc_f16(128, 32, false, false);
+        while (next_piece(p)) {
+          const int n_st = stages_of(p);
+          if (n_st == 0) continue;
+          const uint32_t id = p.ncols <= 16 ? idS16 : idS32;
+          const int qb = np % C::QBUF;
+          const uint64_t q_desc = smem_desc(smem_u32(q_s + qb * C::QTILE), 16, 1024, kSwizzle128);
+          wait(&q_full[qb], (np / C::QBUF) & 1);
+          for (int i = 0; i < n_st; ++i, ++stage) {
+            if (stage >= 2) wait(&s_empty[stage & 1], ((stage >> 1) - 1) & 1);
+            wait(&k_full[stage % C::NK], (stage / C::NK) & 1);
+            if (!alive) continue;
+            tc_fence_after();
+            const uint32_t d = tmem + C::TM_S + (stage & 1) * 32;
+            const uint32_t k0 = tmem + C::TM_K + (stage % C::NK) * 64;
+            if (one) {
 #pragma unroll
               for (int k = 0; k < 8; ++k)
-                tc_mma_ts(tmem + C::TM_S + (stage & 1) * 32,
-                          tmem + C::TM_K + (stage % C::NK) * 64 + k * 8,
-                          smem_desc(qbase + (k >> 2) * C::QHALF + (k & 3) * 32, 16, 1024,
-                                    kSwizzle128),
-                          id, k > 0);
+                tc_mma_ts(d, k0 + k * 8, q_desc + (((k >> 2) * C::QHALF + (k & 3) * 32) >> 4), id,
+                          k > 0);
               tc_commit(&k_empty[stage % C::NK]);
               tc_commit(&s_full[stage & 1]);
             }
-            tc_commit(&q_empty[qb]);
-            ++np;
+            __syncwarp();
           }
-        } else {
-          constexpr uint32_t idP16 = idesc_f16(128, 16, true, true);
-          constexpr uint32_t idP32 = idesc_f16(128, 32, true, true);
-          while (next_piece(p)) {
-            const int n_st = stages_of(p);
-            if (n_st == 0) continue;
-            const uint32_t id = p.ncols <= 16 ? idP16 : idP32;
-            if (np > 0) wait(o_free, (np - 1) & 1);
-            for (int i = 0; i < n_st; ++i, ++stage) {
-              const int b = stage % C::NV;
-              wait(&v_full[b], (stage / C::NV) & 1);
-              wait(&p_full[b], (stage / C::NV) & 1);
-              if (!alive) continue;
-              tc_fence_after();
-              const int nvalid = min(p.tok_end - (p.b0 * B + i * C::TS), C::TS);
-              const int nk = (nvalid + 15) >> 4;
-              const uint32_t vs = smem_u32(v_st + b * C::VBUF), ps = smem_u32(p_st + b * C::PBUF);
-              for (int k = 0; k < nk; ++k)
-                tc_mma(tmem + C::TM_O, smem_desc(vs + k * 2048, C::HALF, 1024, kSwizzle128),
-                       smem_desc(ps + k * 2048, C::PBUF, 1024, kSwizzle128), id,
-                       (i > 0 || k > 0) ? 1u : 0u);
-              tc_commit(&pv_done[b]);
-            }
-            ++np;
-          }
+          if (one) tc_commit(&q_empty[qb]);
+          ++np;
         }
-        // every MMA either thread issued has completed before TMEM is released
+      } else {
+        constexpr uint32_t idP16 = idesc_f16(128, 16, true, true);
+        constexpr uint32_t idP32 = idesc_f16(128, 32, true, true);
+        const uint64_t v_desc = smem_desc(smem_u32(v_st), C::HALF, 1024, kSwizzle128);
+        const uint64_t p_desc = smem_desc(smem_u32(p_st), C::PBUF, 512, kSwizzle64);
+        while (next_piece(p)) {
+          const int n_st = stages_of(p);
+          if (n_st == 0) continue;
+          const uint32_t id = p.ncols <= 16 ? idP16 : idP32;
+          if (np > 0) wait(o_free, (np - 1) & 1);
+          for (int i = 0; i < n_st; ++i, ++stage) {
+            const int b = stage % C::NV, pb = stage % C::NP;
+            wait(&v_full[b], (stage / C::NV) & 1);
+            wait(&p_full[pb], (stage / C::NP) & 1);
+            if (!alive) continue;
+            tc_fence_after();
+            const uint64_t vd = v_desc + ((b * C::VBUF) >> 4), pd = p_desc + ((pb * C::PBUF) >> 4);
+            const int nvalid = p.tok_end - (p.b0 * B + i * C::TS);
+            if (one) {
+              // a stage's 16-token steps; those past the context are left out
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                if (k * 16 < nvalid)
+                  tc_mma(tmem + C::TM_O, vd + k * (2048 >> 4), pd + k * (1024 >> 4), id,
+                         (i > 0 || k > 0) ? 1u : 0u);
+              tc_commit(&pv_done[pb]);
+            }
+            __syncwarp();
+          }
+          ++np;
+        }
+      }
+      // every MMA either warp issued has completed before TMEM is released
+      if (one) {
         tc_commit(fin);
-        mbar_wait_bounded(fin, 0, kWaitLimitNs);
+        q4_wait(fin, 0);
       }
       __syncwarp();
     }
