@@ -10,162 +10,231 @@ namespace pkv {
 
 namespace {
 
-// Slot write into a q4_0 pool: one CTA per (token, layer).  Four lanes share a
-// group of 32 bfloat16 values, eight each (one 16-byte load): the group's
-// largest |x| by two shuffles, d = the fp16 nearest to it over 7 (float32 IEEE
-// division), codes = the integers nearest to x / d (float32 IEEE division,
-// ties to even) clamped to [-7, 7], stored as c + 8, zero when d is 0.  A
-// lane's eight nibbles are one 32-bit word, a group's four words its 16 bytes
-// of the chunk's code plane.
+// x / d rounded to float32 (IEEE) and then to the nearest integer, ties to
+// even, as the format asks, without the division where its rounding cannot
+// show: r = x * (1 / d) is within 2^-22 |x / d| of the rounded quotient, and
+// |x / d| <= 10.5 by the choice of d (a subnormal scale may be rounded down by a
+// third), so both round to the same integer unless r lies within 1e-5 of a
+// half.
+__device__ __forceinline__ float q4_quotient(float x, float d, float inv) {
+  const float r = x * inv, c = rintf(r);
+  if (fabsf(fabsf(r - c) - 0.5f) > 1e-5f) return c;
+  return rintf(__fdiv_rn(x, d));
+}
+
+// Slot write into a q4_0 pool.  Four lanes share a group of 32 bfloat16
+// values, eight each (one 16-byte load): the group's largest |x| by two
+// shuffles, d = the fp16 nearest to it over 7 (float32 IEEE division), codes =
+// the integers nearest to x / d clamped to [-7, 7], stored as c + 8, zero when
+// d is 0.  A lane's eight nibbles are one 32-bit word, a group's four words its
+// 16 bytes of the chunk's code plane.  What bounds it is latency: slot, values
+// and stores depend on each other, so a CTA takes up to kWriteTokens tokens of
+// a layer and every lane has the loads of all of them in flight at once (128
+// tokens into 36 layers: 17 us with one token a CTA).
+constexpr int kWriteTokens = 4;
+
 __global__ void __launch_bounds__(256)
     slot_write_q4_kernel(const uint4* __restrict__ k_new, const uint4* __restrict__ v_new,
-                         const int64_t* __restrict__ slots, int n_tok, unsigned char* kc,
-                         unsigned char* vc, int layer, int n_blocks, int B, int H, int GR,
-                         int32_t* status) {
+                         const int64_t* __restrict__ slots, int n_tok, int per_cta,
+                         unsigned char* kc, unsigned char* vc, int layer, int n_blocks, int B,
+                         int H, int GR, int32_t* status) {
   griddep_wait();
   griddep_launch_dependents();
-  const int i = blockIdx.x;
+  const int i0 = blockIdx.x * per_cta;
   const int ly = layer >= 0 ? layer : blockIdx.y;
-  const int64_t slot = slots[i];
-  if (slot < 0) return;
-  if (slot >= static_cast<int64_t>(n_blocks) * B) {
-    if (threadIdx.x == 0) record_status(status, KV_DEV_BAD_SLOT);
-    return;
-  }
   const int row = H * GR * 4;  // lanes (8-value vectors) of a token row
-  const long long src = ((layer >= 0 ? 0LL : (long long)blockIdx.y * n_tok) + i) * row;
-  const int blk = static_cast<int>(slot / B);
-  const int o = static_cast<int>(slot - static_cast<int64_t>(blk) * B);
+  const long long src = ((layer >= 0 ? 0LL : (long long)blockIdx.y * n_tok) + i0) * row;
+  const int64_t n_slots = static_cast<int64_t>(n_blocks) * B;
   const long long chunk_bytes = static_cast<long long>(B) * GR * 18;
-  const long long blk0 = (static_cast<long long>(ly) * n_blocks + blk) * H;
+  const unsigned quad = 0xfu << (threadIdx.x & 28);
   // K lanes, then V lanes: both multiples of 4, so a group's lanes run together
   for (int v = threadIdx.x; v < 2 * row; v += blockDim.x) {
-    const unsigned quad = 0xfu << (threadIdx.x & 28);
     const bool is_k = v < row;
     const int vv = is_k ? v : v - row;
-    const uint4 x = (is_k ? k_new : v_new)[src + vv];
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    float f[8];
+    const uint4* in = (is_k ? k_new : v_new) + src + vv;
+    uint4 x[kWriteTokens];
+    int64_t slot[kWriteTokens];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      f[2 * k] = __uint_as_float(w[k] << 16);
-      f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-    }
-    float amax = 0.f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(f[k]));
-    amax = fmaxf(amax, __shfl_xor_sync(quad, amax, 1));
-    amax = fmaxf(amax, __shfl_xor_sync(quad, amax, 2));
-    const __half d16 = __float2half_rn(__fdiv_rn(amax, 7.f));
-    const float d = __half2float(d16);
-    uint32_t word = 0;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      float c = d > 0.f ? rintf(__fdiv_rn(f[k], d)) : 0.f;
-      c = fminf(fmaxf(c, -7.f), 7.f);
-      word |= static_cast<uint32_t>(static_cast<int>(c) + 8) << (4 * k);
+    for (int u = 0; u < kWriteTokens; ++u) {
+      if (u >= per_cta || i0 + u >= n_tok) continue;
+      slot[u] = slots[i0 + u];
+      x[u] = in[static_cast<long long>(u) * row];
     }
     const int gi = vv >> 2;  // group of the token row
     const int h = gi / GR, q = gi - h * GR;
-    unsigned char* chunk = (is_k ? kc : vc) + (blk0 + h) * chunk_bytes;
-    reinterpret_cast<uint32_t*>(chunk + (static_cast<long long>(q) * B + o) * 16)[vv & 3] = word;
-    if ((vv & 3) == 0) {
-      __half* sc = reinterpret_cast<__half*>(chunk + static_cast<long long>(GR) * B * 16);
-      sc[is_k ? o * GR + q : q * B + o] = d16;
+#pragma unroll
+    for (int u = 0; u < kWriteTokens; ++u) {
+      if (u >= per_cta || i0 + u >= n_tok || slot[u] < 0) continue;
+      if (slot[u] >= n_slots) {
+        if (threadIdx.x == 0) record_status(status, KV_DEV_BAD_SLOT);
+        continue;
+      }
+      const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+      float f[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        f[2 * k] = __uint_as_float(w[k] << 16);
+        f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+      }
+      float amax = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(f[k]));
+      amax = fmaxf(amax, __shfl_xor_sync(quad, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(quad, amax, 2));
+      const __half d16 = __float2half_rn(__fdiv_rn(amax, 7.f));
+      const float d = __half2float(d16);
+      const float inv = __frcp_rn(d);
+      uint32_t word = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        float c = d > 0.f ? q4_quotient(f[k], d, inv) : 0.f;
+        c = fminf(fmaxf(c, -7.f), 7.f);
+        word |= static_cast<uint32_t>(static_cast<int>(c) + 8) << (4 * k);
+      }
+      const uint32_t blk = static_cast<uint32_t>(slot[u]) / static_cast<uint32_t>(B);
+      const int o = static_cast<int>(static_cast<uint32_t>(slot[u]) - blk * B);
+      unsigned char* chunk =
+          (is_k ? kc : vc) + ((static_cast<long long>(ly) * n_blocks + blk) * H + h) * chunk_bytes;
+      reinterpret_cast<uint32_t*>(chunk + (static_cast<long long>(q) * B + o) * 16)[vv & 3] = word;
+      if ((vv & 3) == 0) {
+        __half* sc = reinterpret_cast<__half*>(chunk + static_cast<long long>(GR) * B * 16);
+        sc[is_k ? o * GR + q : q * B + o] = d16;
+      }
     }
   }
 }
 
-// Four consecutive values of a row as float32.
+// Eight (float32 pools: four) consecutive values of a row as float32.
 template <int DT>
 struct RowSource {
-  const unsigned char* cache;  // K or V
-  const unsigned char* scales; // q8_0
-  float scale;                 // FP8
+  static constexpr int VEC = DT == KV_DTYPE_F32 ? 4 : 8;
+  const unsigned char* cache;   // K or V
+  const unsigned char* scales;  // q8_0
+  float scale;                  // FP8
   int B, H, D, GR;
   bool is_k;
 
-  // values 4 v .. 4 v + 3 of the row [H][D] at (block index incl. layer, offset)
-  __device__ __forceinline__ void load4(long long blk, int o, int v, float (&f)[4]) const {
-    const long long row = (blk * B + o) * H * D;
+  // vector v of the row [H][D] at (block index incl. layer, offset)
+  __device__ __forceinline__ void load(long long blk, int o, int v, float (&f)[VEC]) const {
+    const long long row = (blk * B + o) * H * D / VEC + v;
     if constexpr (DT == KV_DTYPE_F32) {
-      const float4 x = reinterpret_cast<const float4*>(cache)[row / 4 + v];
+      const float4 x = reinterpret_cast<const float4*>(cache)[row];
       f[0] = x.x;
       f[1] = x.y;
       f[2] = x.z;
       f[3] = x.w;
     } else if constexpr (DT == KV_DTYPE_BF16) {
-      const uint2 x = reinterpret_cast<const uint2*>(cache)[row / 4 + v];
-      f[0] = __uint_as_float(x.x << 16);
-      f[1] = __uint_as_float(x.x & 0xffff0000u);
-      f[2] = __uint_as_float(x.y << 16);
-      f[3] = __uint_as_float(x.y & 0xffff0000u);
-    } else if constexpr (DT == KV_DTYPE_FP8_E4M3) {
-      const uint32_t x = reinterpret_cast<const uint32_t*>(cache)[row / 4 + v];
+      const uint4 x = reinterpret_cast<const uint4*>(cache)[row];
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+      for (int k = 0; k < 4; ++k) {
+        f[2 * k] = __uint_as_float(w[k] << 16);
+        f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+      }
+    } else if constexpr (DT == KV_DTYPE_FP8_E4M3) {
+      const uint2 x = reinterpret_cast<const uint2*>(cache)[row];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
         uint32_t h2;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(x >> (16 * k))));
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;"
+            : "=r"(h2)
+            : "h"(static_cast<uint16_t>((k < 2 ? x.x : x.y) >> (16 * (k & 1)))));
         f[2 * k] = scale * __half2float(__ushort_as_half(static_cast<unsigned short>(h2 & 0xffffu)));
         f[2 * k + 1] = scale * __half2float(__ushort_as_half(static_cast<unsigned short>(h2 >> 16)));
       }
     } else if constexpr (DT == KV_DTYPE_Q8_0) {
-      const uint32_t x = reinterpret_cast<const uint32_t*>(cache)[row / 4 + v];
-      const int gi = v >> 3, h = gi / GR, q = gi - h * GR;
+      const uint2 x = reinterpret_cast<const uint2*>(cache)[row];
+      const int gi = v >> 2, h = gi / GR, q = gi - h * GR;
       const float d = __half2float(
           reinterpret_cast<const __half*>(scales)[((blk * H + h) * B + o) * GR + q]);
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        f[k] = d * static_cast<float>(static_cast<int8_t>((x >> (8 * k)) & 0xffu));
+      for (int k = 0; k < 8; ++k)
+        f[k] = d * static_cast<float>(static_cast<int8_t>(((k < 4 ? x.x : x.y) >> (8 * (k & 3))) & 0xffu));
     } else {
-      const int gi = v >> 3, h = gi / GR, q = gi - h * GR;
+      const int gi = v >> 2, h = gi / GR, q = gi - h * GR;
       const unsigned char* chunk = cache + (blk * H + h) * (static_cast<long long>(B) * GR * 18);
-      const uint32_t x = reinterpret_cast<const uint16_t*>(
-          chunk + (static_cast<long long>(q) * B + o) * 16)[v & 7];
+      const uint32_t x = reinterpret_cast<const uint32_t*>(
+          chunk + (static_cast<long long>(q) * B + o) * 16)[v & 3];
       const float d = __half2float(reinterpret_cast<const __half*>(
           chunk + static_cast<long long>(GR) * B * 16)[is_k ? o * GR + q : q * B + o]);
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+      for (int k = 0; k < 8; ++k)
         f[k] = d * static_cast<float>(static_cast<int>((x >> (4 * k)) & 15u) - 8);
     }
   }
 };
 
-// Rows at the listed slots: one CTA per (token, layer), four values a thread.
+// Rows at the listed slots: up to kGatherTokens tokens of a layer a CTA, one
+// vector of a token a thread, the tokens' loads in flight together (as in the
+// slot write).
+constexpr int kGatherTokens = 4;
+
 template <int DT, bool BF16>
 __global__ void __launch_bounds__(256)
     gather_rows_kernel(RowSource<DT> ks, RowSource<DT> vs, const int64_t* __restrict__ slots,
-                       int n_tok, int layer, int n_blocks, void* k_out, void* v_out,
+                       int n_tok, int per_cta, int layer, int n_blocks, void* k_out, void* v_out,
                        int32_t* status) {
+  constexpr int VEC = RowSource<DT>::VEC;
   griddep_wait();
   griddep_launch_dependents();
-  const int i = blockIdx.x;
+  const int i0 = blockIdx.x * per_cta;
   const int ly = layer >= 0 ? layer : blockIdx.y;
-  const int64_t slot = slots[i];
-  if (slot < 0) return;
-  if (slot >= static_cast<int64_t>(n_blocks) * ks.B) {
-    if (threadIdx.x == 0) record_status(status, KV_DEV_BAD_SLOT);
-    return;
-  }
-  const long long blk = static_cast<long long>(ly) * n_blocks + slot / ks.B;
-  const int o = static_cast<int>(slot % ks.B);
-  const int row = ks.H * ks.D / 4;
-  const long long dst = ((layer >= 0 ? 0LL : (long long)blockIdx.y * n_tok) + i) * row;
+  const int64_t n_slots = static_cast<int64_t>(n_blocks) * ks.B;
+  const int row = ks.H * ks.D / VEC;
+  const long long dst = ((layer >= 0 ? 0LL : (long long)blockIdx.y * n_tok) + i0) * row;
   for (int v = threadIdx.x; v < 2 * row; v += blockDim.x) {
     const bool is_k = v < row;
     const int vv = is_k ? v : v - row;
-    float f[4];
-    (is_k ? ks : vs).load4(blk, o, vv, f);
+    const RowSource<DT>& src = is_k ? ks : vs;
+    int64_t slot[kGatherTokens];
+    float f[kGatherTokens][VEC];
+#pragma unroll
+    for (int u = 0; u < kGatherTokens; ++u)
+      slot[u] = u < per_cta && i0 + u < n_tok ? slots[i0 + u] : -1;
+#pragma unroll
+    for (int u = 0; u < kGatherTokens; ++u) {
+      if (slot[u] >= n_slots) {
+        if (threadIdx.x == 0) record_status(status, KV_DEV_BAD_SLOT);
+        slot[u] = -1;
+      }
+      if (slot[u] < 0) continue;
+      const uint32_t blk = static_cast<uint32_t>(slot[u]) / static_cast<uint32_t>(ks.B);
+      src.load(static_cast<long long>(ly) * n_blocks + blk,
+               static_cast<int>(static_cast<uint32_t>(slot[u]) - blk * ks.B), vv, f[u]);
+    }
     void* out = is_k ? k_out : v_out;
-    if constexpr (BF16) {
-      const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]);
-      const __nv_bfloat162 b = __floats2bfloat162_rn(f[2], f[3]);
-      reinterpret_cast<uint2*>(out)[dst + vv] =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-    } else {
-      reinterpret_cast<float4*>(out)[dst + vv] = make_float4(f[0], f[1], f[2], f[3]);
+#pragma unroll
+    for (int u = 0; u < kGatherTokens; ++u) {
+      if (slot[u] < 0) continue;
+      const long long at = dst + static_cast<long long>(u) * row + vv;
+      if constexpr (BF16) {
+        uint32_t w[VEC / 2];
+#pragma unroll
+        for (int k = 0; k < VEC / 2; ++k) {
+          const __nv_bfloat162 a = __floats2bfloat162_rn(f[u][2 * k], f[u][2 * k + 1]);
+          w[k] = *reinterpret_cast<const uint32_t*>(&a);
+        }
+        if constexpr (VEC == 8)
+          reinterpret_cast<uint4*>(out)[at] = make_uint4(w[0], w[1], w[2], w[3]);
+        else
+          reinterpret_cast<uint2*>(out)[at] = make_uint2(w[0], w[1]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < VEC / 4; ++k)
+          reinterpret_cast<float4*>(out)[at * (VEC / 4) + k] =
+              make_float4(f[u][4 * k], f[u][4 * k + 1], f[u][4 * k + 2], f[u][4 * k + 3]);
+      }
     }
   }
+}
+
+// Tokens per CTA: several where that still leaves the SMs two CTAs each.
+int tokens_per_cta(const kvPool* p, int n_tokens, int layer, int most) {
+  const long long rows = static_cast<long long>(n_tokens) * (layer >= 0 ? 1 : p->L);
+  const int sms = p->sm_count > 0 ? p->sm_count : 1;
+  int n = most;
+  while (n > 1 && rows < 2LL * sms * n) n >>= 1;
+  return n;
 }
 
 template <int DT>
@@ -177,14 +246,15 @@ cudaError_t launch_gather(const kvPool* p, int layer, const int64_t* slots, int 
   RowSource<DT> vs{static_cast<const unsigned char*>(p->v),
                    static_cast<const unsigned char*>(p->v_sc), p->v_scale, p->B, p->H, p->D,
                    p->D / 32, false};
-  const int lanes = 2 * p->H * p->D / 4;
+  const int lanes = 2 * p->H * p->D / RowSource<DT>::VEC;
   const int threads = lanes >= 256 ? 256 : (lanes + 31) / 32 * 32;
-  const dim3 grid(n_tokens, layer >= 0 ? 1 : p->L);
+  const int per_cta = tokens_per_cta(p, n_tokens, layer, kGatherTokens);
+  const dim3 grid((n_tokens + per_cta - 1) / per_cta, layer >= 0 ? 1 : p->L);
   return launch_kernel(p->pdl,
                        out_dtype == KV_DTYPE_BF16 ? gather_rows_kernel<DT, true>
                                                   : gather_rows_kernel<DT, false>,
-                       grid, dim3(threads), 0, st, ks, vs, slots, n_tokens, layer, p->N, k_out,
-                       v_out, p->d_status);
+                       grid, dim3(threads), 0, st, ks, vs, slots, n_tokens, per_cta, layer, p->N,
+                       k_out, v_out, p->d_status);
 }
 
 // Staged chunked prefill of a q4_0 pool, first kernel: one CTA per (K/V head,
@@ -194,7 +264,7 @@ cudaError_t launch_gather(const kvPool* p, int layer, const int64_t* slots, int 
 // floor(log2 d) - 11 keeps every copied value below 2^15 and the values down
 // to 2^-29 of that normal in fp16, whatever the magnitude of K and V.  Reads
 // the scales alone (a ninth of the blocks' bytes).
-constexpr int kScaleThreads = 512;
+constexpr int kScaleThreads = 512, kScaleAhead = 8;
 
 __global__ void __launch_bounds__(kScaleThreads)
     prefill_scale_q4_kernel(const unsigned char* __restrict__ kc,
@@ -211,23 +281,41 @@ __global__ void __launch_bounds__(kScaleThreads)
   if (nb > g.max_blocks) nb = g.max_blocks;
   uint32_t mk = 0, mv = 0;
   const long long total = static_cast<long long>(nb) * vecs;
-  for (long long w = threadIdx.x; w < total; w += kScaleThreads) {
-    const int j = static_cast<int>(w / vecs), v = static_cast<int>(w - static_cast<long long>(j) * vecs);
-    const int pid = g.table[static_cast<long long>(i) * g.max_blocks + j];
-    if (pid < 0 || pid >= n_blocks) continue;  // flagged by the copy
-    const long long off = ((static_cast<long long>(g.layer) * n_blocks + pid) * H + h) * chunk_bytes +
-                          static_cast<long long>(GR) * B * 16;
-    const uint4 xk = reinterpret_cast<const uint4*>(kc + off)[v];
-    const uint4 xv = reinterpret_cast<const uint4*>(vc + off)[v];
-    const uint32_t wk[4] = {xk.x, xk.y, xk.z, xk.w}, wv[4] = {xv.x, xv.y, xv.z, xv.w};
-    const int rows = len - j * B;  // slots of this block inside the context
+  // kScaleAhead vectors of K and of V in flight a thread
+  const int32_t* row = g.table + static_cast<long long>(i) * g.max_blocks;
+  for (long long w0 = threadIdx.x; w0 < total; w0 += kScaleThreads * kScaleAhead) {
+    int pid[kScaleAhead], j[kScaleAhead], v[kScaleAhead];
+    uint4 xk[kScaleAhead], xv[kScaleAhead];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int o = v * 8 + e;
-      const uint32_t bk = (wk[e >> 1] >> (16 * (e & 1))) & 0x7fffu;
-      const uint32_t bv = (wv[e >> 1] >> (16 * (e & 1))) & 0x7fffu;
-      if (o / GR < rows) mk = max(mk, bk);  // K: [B][GR]
-      if (o % B < rows) mv = max(mv, bv);   // V: [GR][B]
+    for (int u = 0; u < kScaleAhead; ++u) {
+      const long long w = w0 + static_cast<long long>(u) * kScaleThreads;
+      j[u] = static_cast<int>(w / vecs);
+      v[u] = static_cast<int>(w - static_cast<long long>(j[u]) * vecs);
+      pid[u] = w < total ? row[j[u]] : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < kScaleAhead; ++u) {
+      if (pid[u] < 0 || pid[u] >= n_blocks) continue;  // flagged by the copy
+      const long long off =
+          ((static_cast<long long>(g.layer) * n_blocks + pid[u]) * H + h) * chunk_bytes +
+          static_cast<long long>(GR) * B * 16;
+      xk[u] = reinterpret_cast<const uint4*>(kc + off)[v[u]];
+      xv[u] = reinterpret_cast<const uint4*>(vc + off)[v[u]];
+    }
+#pragma unroll
+    for (int u = 0; u < kScaleAhead; ++u) {
+      if (pid[u] < 0 || pid[u] >= n_blocks) continue;
+      const uint32_t wk[4] = {xk[u].x, xk[u].y, xk[u].z, xk[u].w};
+      const uint32_t wv[4] = {xv[u].x, xv[u].y, xv[u].z, xv[u].w};
+      const int rows = len - j[u] * B;  // slots of this block inside the context
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int o = v[u] * 8 + e;
+        const uint32_t bk = (wk[e >> 1] >> (16 * (e & 1))) & 0x7fffu;
+        const uint32_t bv = (wv[e >> 1] >> (16 * (e & 1))) & 0x7fffu;
+        if (o / GR < rows) mk = max(mk, bk);  // K: [B][GR]
+        if (o % B < rows) mv = max(mv, bv);   // V: [GR][B]
+      }
     }
   }
 #pragma unroll
@@ -327,10 +415,11 @@ cudaError_t launch_slot_write_q4(const kvPool* p, int layer, const void* k_new, 
                                  const int64_t* slots, int n_tokens, cudaStream_t st) {
   const int lanes = 2 * p->H * p->D / 8;
   const int threads = lanes >= 256 ? 256 : (lanes + 31) / 32 * 32;
-  const dim3 grid(n_tokens, layer >= 0 ? 1 : p->L);
+  const int per_cta = tokens_per_cta(p, n_tokens, layer, kWriteTokens);
+  const dim3 grid((n_tokens + per_cta - 1) / per_cta, layer >= 0 ? 1 : p->L);
   return launch_kernel(p->pdl, slot_write_q4_kernel, grid, dim3(threads), 0, st,
                        static_cast<const uint4*>(k_new), static_cast<const uint4*>(v_new), slots,
-                       n_tokens, static_cast<unsigned char*>(p->k),
+                       n_tokens, per_cta, static_cast<unsigned char*>(p->k),
                        static_cast<unsigned char*>(p->v), layer, p->N, p->B, p->H, p->D / 32,
                        p->d_status);
 }

@@ -18,7 +18,7 @@ namespace pkv {
 namespace {
 
 constexpr int kScanThreads = 1024;
-constexpr int kFillThreads = 256;
+constexpr int kFillThreads = 256, kFillAhead = 4;
 constexpr int kMaxRows = 1 << 20;  // rows of a table set: one bit each in shared memory
 
 // Workspace: the batch's verdict and the ring position it starts at, then one
@@ -241,15 +241,22 @@ __global__ void __launch_bounds__(kFillThreads) tables_fill_kernel(const TablesA
   int32_t* row = live ? a.tables + static_cast<int64_t>(r) * a.max_blocks : nullptr;
   int32_t* out = a.block_table ? a.block_table + static_cast<int64_t>(i) * a.max_blocks : nullptr;
   const int j0 = out ? 0 : ob, j1 = out ? a.max_blocks : nb;
-  for (int j = j0 + part * kFillThreads + threadIdx.x; j < j1; j += parts * kFillThreads) {
-    int id = -1;
-    if (j < ob) {
-      id = row[j];
-    } else if (j < nb) {
-      id = taken(a, h.head, p.blk0 + j - ob);
-      row[j] = id;
+  // kFillAhead entries a thread, their loads in flight together
+  for (int jb = j0 + part * kFillThreads * kFillAhead + threadIdx.x; jb < j1;
+       jb += parts * kFillThreads * kFillAhead) {
+    int id[kFillAhead];
+#pragma unroll
+    for (int u = 0; u < kFillAhead; ++u) {
+      const int j = jb + u * kFillThreads;
+      id[u] = j < ob ? row[j] : (j < nb ? taken(a, h.head, p.blk0 + j - ob) : -1);
     }
-    if (out) out[j] = id;
+#pragma unroll
+    for (int u = 0; u < kFillAhead; ++u) {
+      const int j = jb + u * kFillThreads;
+      if (j >= j1) continue;
+      if (j >= ob && j < nb) row[j] = id[u];
+      if (out) out[j] = id[u];
+    }
   }
 }
 
@@ -322,9 +329,10 @@ cudaError_t launch_scan(bool pdl, const TablesArgs& a, cudaStream_t st) {
   return launch_kernel(pdl, tables_scan_kernel<RELEASE>, dim3(1), dim3(kScanThreads), smem, st, a);
 }
 
-// CTAs per row: enough that a wide table is spread, at most eight.
+// CTAs per row: one for each kFillAhead * kFillThreads entries, at most eight.
 int row_parts(int max_blocks) {
-  const int want = (max_blocks + 4 * kFillThreads - 1) / (4 * kFillThreads);
+  const int per = kFillAhead * kFillThreads;
+  const int want = (max_blocks + per - 1) / per;
   return want < 1 ? 1 : (want > 8 ? 8 : want);
 }
 
