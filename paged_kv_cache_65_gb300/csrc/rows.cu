@@ -10,16 +10,36 @@ namespace pkv {
 
 namespace {
 
-// x / d rounded to float32 (IEEE) and then to the nearest integer, ties to
-// even, as the format asks, without the division where its rounding cannot
-// show: r = x * (1 / d) is within 2^-22 |x / d| of the rounded quotient, and
-// |x / d| <= 10.5 by the choice of d (a subnormal scale may be rounded down by a
-// third), so both round to the same integer unless r lies within 1e-5 of a
-// half.
-__device__ __forceinline__ float q4_quotient(float x, float d, float inv) {
-  const float r = x * inv, c = rintf(r);
-  if (fabsf(fabsf(r - c) - 0.5f) > 1e-5f) return c;
-  return rintf(__fdiv_rn(x, d));
+// Codes of eight values as one 32-bit word of nibbles c + 8.  The format asks
+// for x / d rounded to float32 (IEEE) and then to the nearest integer, ties to
+// even.  r = x * inv is within 2^-21 |x / d| of that quotient, and |x / d| <=
+// 10.5 by the choice of d (a subnormal scale may be rounded down by a third),
+// so both round to the same integer unless r lies within 1e-5 of a half: only
+// then are the eight divided out.  Rounding is the addition of 1.5 * 2^23,
+// whose sum holds the integer in its low bits; four nibbles are joined by
+// multiply-adds (exact below 2^24), so no conversion instruction is needed.
+__device__ __forceinline__ uint32_t q4_codes8(const float (&f)[8], float d, float inv) {
+  constexpr float kRound = 12582912.f;  // 1.5 * 2^23
+  float c[8];
+  float off = 0.f;  // largest distance from the integer taken
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float r = f[k] * inv;
+    c[k] = __fadd_rn(r, kRound) - kRound;
+    off = fmaxf(off, fabsf(r - c[k]));
+  }
+  if (!(off < 0.49999f)) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) c[k] = d > 0.f ? rintf(__fdiv_rn(f[k], d)) : 0.f;
+  }
+  float lo = 0.f, hi = 0.f;
+#pragma unroll
+  for (int k = 3; k >= 0; --k) {
+    lo = fmaf(lo, 16.f, fminf(fmaxf(c[k], -7.f), 7.f) + 8.f);
+    hi = fmaf(hi, 16.f, fminf(fmaxf(c[k + 4], -7.f), 7.f) + 8.f);
+  }
+  // 2^23 + n holds n < 2^16 in its low half
+  return __byte_perm(__float_as_uint(lo + 8388608.f), __float_as_uint(hi + 8388608.f), 0x5410);
 }
 
 // Slot write into a q4_0 pool.  Four lanes share a group of 32 bfloat16
@@ -31,7 +51,7 @@ __device__ __forceinline__ float q4_quotient(float x, float d, float inv) {
 // and stores depend on each other, so a CTA takes up to kWriteTokens tokens of
 // a layer and every lane has the loads of all of them in flight at once (128
 // tokens into 36 layers: 17 us with one token a CTA).
-constexpr int kWriteTokens = 4;
+constexpr int kWriteTokens = 2;
 
 __global__ void __launch_bounds__(256)
     slot_write_q4_kernel(const uint4* __restrict__ k_new, const uint4* __restrict__ v_new,
@@ -83,14 +103,7 @@ __global__ void __launch_bounds__(256)
       amax = fmaxf(amax, __shfl_xor_sync(quad, amax, 2));
       const __half d16 = __float2half_rn(__fdiv_rn(amax, 7.f));
       const float d = __half2float(d16);
-      const float inv = __frcp_rn(d);
-      uint32_t word = 0;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        float c = d > 0.f ? q4_quotient(f[k], d, inv) : 0.f;
-        c = fminf(fmaxf(c, -7.f), 7.f);
-        word |= static_cast<uint32_t>(static_cast<int>(c) + 8) << (4 * k);
-      }
+      const uint32_t word = d > 0.f ? q4_codes8(f, d, __fdividef(1.f, d)) : 0x88888888u;
       const uint32_t blk = static_cast<uint32_t>(slot[u]) / static_cast<uint32_t>(B);
       const int o = static_cast<int>(static_cast<uint32_t>(slot[u]) - blk * B);
       unsigned char* chunk =
@@ -159,71 +172,56 @@ struct RowSource {
           chunk + static_cast<long long>(GR) * B * 16)[is_k ? o * GR + q : q * B + o]);
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        f[k] = d * static_cast<float>(static_cast<int>((x >> (4 * k)) & 15u) - 8);
+        // 2^23 + n - (2^23 + 8) = c without a conversion
+        f[k] = d * (__uint_as_float(0x4b000000u | ((x >> (4 * k)) & 15u)) - 8388616.f);
     }
   }
 };
 
-// Rows at the listed slots: up to kGatherTokens tokens of a layer a CTA, one
-// vector of a token a thread, the tokens' loads in flight together (as in the
-// slot write).
-constexpr int kGatherTokens = 4;
-
+// Rows at the listed slots: one token of a layer a CTA, one vector of its K or
+// V row a thread.
 template <int DT, bool BF16>
 __global__ void __launch_bounds__(256)
     gather_rows_kernel(RowSource<DT> ks, RowSource<DT> vs, const int64_t* __restrict__ slots,
-                       int n_tok, int per_cta, int layer, int n_blocks, void* k_out, void* v_out,
+                       int n_tok, int layer, int n_blocks, void* k_out, void* v_out,
                        int32_t* status) {
   constexpr int VEC = RowSource<DT>::VEC;
   griddep_wait();
   griddep_launch_dependents();
-  const int i0 = blockIdx.x * per_cta;
+  const int i = blockIdx.x;
   const int ly = layer >= 0 ? layer : blockIdx.y;
-  const int64_t n_slots = static_cast<int64_t>(n_blocks) * ks.B;
+  const int64_t slot = slots[i];
+  if (slot < 0) return;
+  if (slot >= static_cast<int64_t>(n_blocks) * ks.B) {
+    if (threadIdx.x == 0) record_status(status, KV_DEV_BAD_SLOT);
+    return;
+  }
+  const uint32_t blk = static_cast<uint32_t>(slot) / static_cast<uint32_t>(ks.B);
+  const int o = static_cast<int>(static_cast<uint32_t>(slot) - blk * ks.B);
   const int row = ks.H * ks.D / VEC;
-  const long long dst = ((layer >= 0 ? 0LL : (long long)blockIdx.y * n_tok) + i0) * row;
+  const long long dst = ((layer >= 0 ? 0LL : (long long)blockIdx.y * n_tok) + i) * row;
   for (int v = threadIdx.x; v < 2 * row; v += blockDim.x) {
     const bool is_k = v < row;
     const int vv = is_k ? v : v - row;
-    const RowSource<DT>& src = is_k ? ks : vs;
-    int64_t slot[kGatherTokens];
-    float f[kGatherTokens][VEC];
-#pragma unroll
-    for (int u = 0; u < kGatherTokens; ++u)
-      slot[u] = u < per_cta && i0 + u < n_tok ? slots[i0 + u] : -1;
-#pragma unroll
-    for (int u = 0; u < kGatherTokens; ++u) {
-      if (slot[u] >= n_slots) {
-        if (threadIdx.x == 0) record_status(status, KV_DEV_BAD_SLOT);
-        slot[u] = -1;
-      }
-      if (slot[u] < 0) continue;
-      const uint32_t blk = static_cast<uint32_t>(slot[u]) / static_cast<uint32_t>(ks.B);
-      src.load(static_cast<long long>(ly) * n_blocks + blk,
-               static_cast<int>(static_cast<uint32_t>(slot[u]) - blk * ks.B), vv, f[u]);
-    }
+    float f[VEC];
+    (is_k ? ks : vs).load(static_cast<long long>(ly) * n_blocks + blk, o, vv, f);
     void* out = is_k ? k_out : v_out;
+    if constexpr (BF16) {
+      uint32_t w[VEC / 2];
 #pragma unroll
-    for (int u = 0; u < kGatherTokens; ++u) {
-      if (slot[u] < 0) continue;
-      const long long at = dst + static_cast<long long>(u) * row + vv;
-      if constexpr (BF16) {
-        uint32_t w[VEC / 2];
-#pragma unroll
-        for (int k = 0; k < VEC / 2; ++k) {
-          const __nv_bfloat162 a = __floats2bfloat162_rn(f[u][2 * k], f[u][2 * k + 1]);
-          w[k] = *reinterpret_cast<const uint32_t*>(&a);
-        }
-        if constexpr (VEC == 8)
-          reinterpret_cast<uint4*>(out)[at] = make_uint4(w[0], w[1], w[2], w[3]);
-        else
-          reinterpret_cast<uint2*>(out)[at] = make_uint2(w[0], w[1]);
-      } else {
-#pragma unroll
-        for (int k = 0; k < VEC / 4; ++k)
-          reinterpret_cast<float4*>(out)[at * (VEC / 4) + k] =
-              make_float4(f[u][4 * k], f[u][4 * k + 1], f[u][4 * k + 2], f[u][4 * k + 3]);
+      for (int k = 0; k < VEC / 2; ++k) {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
+        w[k] = *reinterpret_cast<const uint32_t*>(&a);
       }
+      if constexpr (VEC == 8)
+        reinterpret_cast<uint4*>(out)[dst + vv] = make_uint4(w[0], w[1], w[2], w[3]);
+      else
+        reinterpret_cast<uint2*>(out)[dst + vv] = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < VEC / 4; ++k)
+        reinterpret_cast<float4*>(out)[(dst + vv) * (VEC / 4) + k] =
+            make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
     }
   }
 }
@@ -248,13 +246,12 @@ cudaError_t launch_gather(const kvPool* p, int layer, const int64_t* slots, int 
                    p->D / 32, false};
   const int lanes = 2 * p->H * p->D / RowSource<DT>::VEC;
   const int threads = lanes >= 256 ? 256 : (lanes + 31) / 32 * 32;
-  const int per_cta = tokens_per_cta(p, n_tokens, layer, kGatherTokens);
-  const dim3 grid((n_tokens + per_cta - 1) / per_cta, layer >= 0 ? 1 : p->L);
+  const dim3 grid(n_tokens, layer >= 0 ? 1 : p->L);
   return launch_kernel(p->pdl,
                        out_dtype == KV_DTYPE_BF16 ? gather_rows_kernel<DT, true>
                                                   : gather_rows_kernel<DT, false>,
-                       grid, dim3(threads), 0, st, ks, vs, slots, n_tokens, per_cta, layer, p->N,
-                       k_out, v_out, p->d_status);
+                       grid, dim3(threads), 0, st, ks, vs, slots, n_tokens, layer, p->N, k_out, v_out,
+                       p->d_status);
 }
 
 // Staged chunked prefill of a q4_0 pool, first kernel: one CTA per (K/V head,
