@@ -100,13 +100,9 @@ cudaError_t launch_mma_q8(int D, int G, const CUtensorMap& tk, const CUtensorMap
                           cudaStream_t st, bool pdl, bool* supported);
 
 // The pass over a q4_0 pool (4-bit codes, fp16 scales per 32 values, read
-// through a.k_pool / a.v_pool), D_h 64 or 128.
-cudaError_t launch_decode_q4(int D, const DecodeArgs& a, int sm_count, int max_grid, int* grid_io,
-                             cudaStream_t st, bool pdl, bool* supported);
-
-// The tcgen05 pass over a q4_0 pool, D_h = 128; one CTA per SM.
-cudaError_t launch_decode_q4_tc(const DecodeArgs& a, int sm_count, int max_grid, int* grid_io,
-                                cudaStream_t st, bool pdl);
+// through a.k_pool / a.v_pool), D_h 64 or 128, in its narrow or its wide form.
+cudaError_t launch_decode_q4(int D, const DecodeArgs& a, bool wide, int sm_count, int max_grid,
+                             int* grid_io, cudaStream_t st, bool pdl, bool* supported);
 
 // Dispatch over (D, G) for one element size; *supported = false when the
 // shape has no compiled instantiation.

@@ -49,24 +49,34 @@
 
 namespace pkv {
 
-constexpr int kQ4Warps = 4;                        // consumer warps
-constexpr int kQ4Threads = (kQ4Warps + 1) * 32;    // and the producer
-constexpr int kQ4CtasPerSm = 2;
+constexpr int kQ4Warps = 4;  // consumer warps of a team
+
+// A CTA is several teams, each a CTA of the split by itself: four consumer
+// warps (a warpgroup), a producer warp, its own stages and work.  The producers
+// share the last warpgroup.  NTW: 8-column tiles a consumer warp holds at once.
+template <bool WIDE>
+struct Q4Team {
+  static constexpr int TEAMS = WIDE ? 2 : 3;
+  static constexpr int NTW = WIDE ? 2 : 1;
+  static constexpr int NST = WIDE ? 5 : 3;                // stages in a team's ring
+  static constexpr int THREADS = (TEAMS + 1) * 128;
+  // registers a thread: at launch, consumers, producers
+  static constexpr int REGS = WIDE ? 168 : 128, REGS_C = WIDE ? 224 : 152, REGS_P = 56;
+  static_assert(TEAMS * REGS_C + REGS_P <= (TEAMS + 1) * REGS, "setmaxnreg waits for registers");
+};
 
 template <int D>
 struct Q4Cfg {
   static constexpr int GR = D / 32;                // groups of 32 dimensions
-  static constexpr int TS = 64;                    // tokens per slot
+  static constexpr int TS = 128;                   // tokens per stage
   static constexpr int ROW = D / 2 + D / 16;       // bytes per token row: codes and scales
-  static constexpr int SLOT_BYTES = TS * ROW;      // K (or V) per slot
-  static constexpr int NS = 10;                    // slots in the ring
-  static constexpr int PT = 4;                     // 16-token tiles per pass
+  static constexpr int STAGE_BYTES = TS * ROW;     // K (or V) per stage
   static constexpr int MT = D / 16;                // m-tiles of O^T
   static constexpr int CC = 4;                     // columns per combine pass
   static_assert(D == 64 || D == 128, "head dim");
 };
 
-// Tokens per unit: a block when it divides the slot, else the slot (blocks of
+// Tokens per unit: a block when it has at most 64, else 64 (blocks of
 // 128, 192 and 256).  A power of two.
 __host__ __device__ constexpr int q4_unit_rows(int B) { return B < 64 ? B : 64; }
 
@@ -74,25 +84,32 @@ __host__ __device__ constexpr int q4_unit_rows(int B) { return B < 64 ? B : 64; 
 // stands for token q4_srow(k); lane i of ldsm8_t addresses token q4_vrow(i).
 // ldsm8_t hands lane (g, t) the tokens of lanes 4t .. 4t + 3 as bytes 0 .. 3;
 // bytes 0 and 2 become k-slots 2t and 2t + 1, bytes 1 and 3 k-slots 2t + 8 and
-// 2t + 9.  The rotation of the upper eight keeps each 8-lane phase on eight
-// different 16-byte bank groups.
-__device__ __forceinline__ int q4_srow(int k) { return k < 8 ? k : 8 + ((k + 4) & 7); }
-__device__ __forceinline__ int q4_vrow(int i) {
-  return q4_srow(2 * (i >> 2) + ((i >> 1) & 1) + 8 * (i & 1));
-}
+// 2t + 9: tokens 4t .. 4t + 3, whose four V scales are one 8-byte load.
+__device__ __forceinline__ int q4_srow(int k) { return 4 * ((k >> 1) & 3) + 2 * (k >> 3) + (k & 1); }
+__device__ __forceinline__ int q4_vrow(int i) { return (i & ~3) + 2 * (i & 1) + ((i >> 1) & 1); }
 
 constexpr uint32_t kNibLo = 0x000f000fu;  // n * 2^-24
-constexpr uint32_t kNibHi = 0x00f000f0u;  // n * 2^-20
-constexpr uint32_t kNibOffLo = 0x80088008u;  // -8 * 2^-24 twice
-constexpr uint32_t kNibOffHi = 0x80808080u;  // -8 * 2^-20 twice
+constexpr uint32_t kByte = 0x00ff00ffu;   // (16 n' + n) * 2^-24, n' the high nibble
+constexpr uint32_t kOffNib = 0x80088008u;   // -8 * 2^-24 twice
+constexpr uint32_t kOffByte = 0x80888088u;  // -136 * 2^-24 twice
 
-// Headroom of a column's reference over the maximum that moved it, in base-2
-// units: weights are at most 1 and those of the moving maximum 2^-2.
+// Headroom of a column's largest weight over the maximum that set it, in
+// base-2 units: the weights of a moved maximum are 2^(e - kQ4Head), e below.
 constexpr float kQ4Head = 2.f;
+// Weights go up to 2^e: 14 while every V scale seen is below 2 (bit 14 of an
+// fp16), so that a weight times a scale stays in fp16's normal range far below
+// the maximum however small the scales are; 0 from the first larger scale on.
+constexpr float kQ4Exp = 14.f;
 
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 r;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(addr));
   return r;
 }
 
@@ -112,6 +129,8 @@ __device__ __forceinline__ void q4_mma(float (&d)[4], uint32_t a0, uint32_t a1, 
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// Bytes 1 and 3 of a word as halves: the fp16 operands 16 n' + n of them.
+__device__ __forceinline__ uint32_t q4_odd_bytes(uint32_t w) { return __byte_perm(w, 0, 0x4341); }
 // without an addend: D = A . B
 __device__ __forceinline__ void q4_mma_z(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -167,55 +186,52 @@ __device__ __forceinline__ bool q4_wait(uint64_t* bar, uint32_t parity) {
   return true;
 }
 
-// Arrive `n` times.
-__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
-  asm volatile(
-      "{\n\t.reg .b64 st;\n\t"
-      "mbarrier.arrive.release.cta.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
-      "r"(n)
-      : "memory");
-}
-
-template <int D>
-constexpr int decode_q4_smem_bytes() {
+template <int D, bool WIDE>
+constexpr int decode_q4_team_bytes() {
   using C = Q4Cfg<D>;
-  return 2 * C::NS * C::SLOT_BYTES        // K and V stages
-         + kQ4Warps * C::CC * D * 4         // combine: O per warp, CC columns at a time
-         + kQ4Warps * 8 * 2 * 4             // combine: m, l per warp and column
-         + 2 * C::NS * 8                    // mbarriers
-         + kTableCache * 4                  // producer table cache
-         + kPieceRing * (48 + 16)           // piece descriptors and their mbarriers
-         + 64 + 128 + 16;                   // walk state, start record, alignment
+  using T = Q4Team<WIDE>;
+  constexpr int n = 2 * T::NST * C::STAGE_BYTES       // K and V stages
+                    + kQ4Warps * C::CC * D * 4        // combine: O per warp, CC columns at a time
+                    + kQ4Warps * T::NTW * 8 * 2 * 4   // combine: m, l per warp and column
+                    + 2 * T::NST * 8                  // mbarriers
+                    + kTableCache * 4                 // producer table cache
+                    + kPieceRing * (48 + 16)          // piece descriptors and their mbarriers
+                    + 128;                            // start record
+  return (n + 127) / 128 * 128;
 }
 
 // UR: q4_unit_rows of the pool's block size.
-template <int D, int UR, bool PLAN>
-__global__ void __launch_bounds__(kQ4Threads, kQ4CtasPerSm) decode_q4_kernel(const DecodeArgs a) {
+template <int D, int UR, bool PLAN, bool WIDE>
+__global__ void __launch_bounds__(Q4Team<WIDE>::THREADS, 1) decode_q4_kernel(const DecodeArgs a) {
   using C = Q4Cfg<D>;
-  constexpr int NS = C::NS, GR = C::GR, PT = C::PT;
-  extern __shared__ __align__(16) unsigned char smem_raw[];
-  unsigned char* k_st = smem_raw;
-  unsigned char* v_st = k_st + NS * C::SLOT_BYTES;
-  float* cmb_o = reinterpret_cast<float*>(v_st + NS * C::SLOT_BYTES);
-  float* cmb_ml = cmb_o + kQ4Warps * C::CC * D;
-  uint64_t* full = reinterpret_cast<uint64_t*>(cmb_ml + kQ4Warps * 8 * 2);
-  uint64_t* empty = full + NS;
-  long long* walk = reinterpret_cast<long long*>(empty + NS);
-  int32_t* tcache = reinterpret_cast<int32_t*>(walk + 4);
-  PlanStart* rec_s = reinterpret_cast<PlanStart*>(tcache + kTableCache);
-  Piece* ring = reinterpret_cast<Piece*>(rec_s + 1);
-  uint64_t* dfull = reinterpret_cast<uint64_t*>(ring + kPieceRing);
-  uint64_t* dempty = dfull + kPieceRing;
-
-  const int warp = threadIdx.x >> 5;
+  using T = Q4Team<WIDE>;
+  constexpr int NST = T::NST, GR = C::GR, NTW = T::NTW;
+  extern __shared__ __align__(128) unsigned char smem_q4[];
+  const int warp_cta = threadIdx.x >> 5;
+  const bool is_producer = warp_cta >= T::TEAMS * 4;
+  const int team = is_producer ? warp_cta - T::TEAMS * 4 : warp_cta >> 2;
+  const int warp = warp_cta & 3;  // consumer warp of its team
   const int lane = threadIdx.x & 31;
+  const int cta = blockIdx.x * T::TEAMS + team;  // of the split's a.grid
+  unsigned char* k_st = smem_q4 + team * decode_q4_team_bytes<D, WIDE>();
+  unsigned char* v_st = k_st + NST * C::STAGE_BYTES;
+  float* cmb_o = reinterpret_cast<float*>(v_st + NST * C::STAGE_BYTES);
+  float* cmb_ml = cmb_o + kQ4Warps * C::CC * D;
+  uint64_t* full = reinterpret_cast<uint64_t*>(cmb_ml + kQ4Warps * NTW * 8 * 2);
+  uint64_t* empty = full + NST;
+  uint64_t* dfull = empty + NST;
+  uint64_t* dempty = dfull + kPieceRing;
+  PlanStart* rec_s = reinterpret_cast<PlanStart*>(dempty + kPieceRing);
+  Piece* ring = reinterpret_cast<Piece*>(rec_s + 1);
+  int32_t* tcache = reinterpret_cast<int32_t*>(ring + kPieceRing);
+
   const int B = a.block_size;
   const int H = a.n_kv_heads, G = a.n_q_heads / H;
   constexpr int lur = ilog2(UR);
   constexpr uint32_t unit_bytes = static_cast<uint32_t>(UR) * C::ROW;
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < NS; ++i) {
+  if (is_producer && team < T::TEAMS && lane == 0) {
+    for (int i = 0; i < NST; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], kQ4Warps);
     }
@@ -225,75 +241,58 @@ __global__ void __launch_bounds__(kQ4Threads, kQ4CtasPerSm) decode_q4_kernel(con
     }
     fence_barrier_init();
   }
-  // tables and lengths that kernels before this one write (a pool with device
-  // tables) are read only after them; host-written ones before the wait, as in
-  // decode_mma.cuh
-  if (a.meta_wait) griddep_wait();
-  const bool use_rec = PLAN && a.starts != nullptr && a.start_grid == a.grid;
-  if (warp == 0) {
-    if constexpr (PLAN) {
-      const long long W = a.plan_W;
-      long long chunk = (W + a.grid - 1) / a.grid;
-      if (chunk == 0) chunk = 1;
-      int s0 = 0;
-      if (use_rec) {
-        reinterpret_cast<int32_t*>(rec_s)[lane] =
-            reinterpret_cast<const int32_t*>(a.starts + blockIdx.x)[lane];
-      } else {
-        const long long r0 = (long long)blockIdx.x * chunk;
-        s0 = r0 < W ? plan_find(a.segs, a.n_segs, r0) : a.n_segs;
-      }
-      if (lane == 0) {
-        walk[0] = s0;
-        walk[1] = 0;
-        walk[2] = W;
-        walk[3] = chunk;
-      }
-    } else {
-      WalkStart w = find_start(a.ctx, a.n_seq, B, H, a.max_blocks, a.grid, blockIdx.x, a.status);
-      if (lane == 0) {
-        walk[0] = w.s;
-        walk[1] = w.pre;
-        walk[2] = w.W;
-        walk[3] = w.chunk;
-      }
-    }
-  }
   __syncthreads();
 
-  const long long W = walk[2], chunk = walk[3];
-  const long long r_begin = (long long)blockIdx.x * chunk;
-  const long long r_end = r_begin + chunk < W ? r_begin + chunk : W;
   auto wait_previous_grid = [&]() {
     griddep_wait();
     griddep_launch_dependents();
     if constexpr (!PLAN) {
-      if (blockIdx.x == 0 && warp == 0)
+      if (cta == 0 && !is_producer && warp == 0)
         write_prefix(a.ctx, a.n_seq, B, H, a.max_blocks, a.ws_pre);
     }
   };
 
-  if (warp == kQ4Warps) {
+  if (is_producer) {
     // ------------------------------------------------------------ producer
+    reg_dealloc<T::REGS_P>();
+    if (team >= T::TEAMS) return;  // a warp without a team
+    // tables and lengths that kernels before this one write (a pool with device
+    // tables) are read only after them; host-written ones before the wait, as in
+    // decode_mma.cuh
+    if (a.meta_wait) griddep_wait();
+    const bool use_rec = PLAN && a.starts != nullptr && a.start_grid == a.grid;
     PieceWalker pw;
     PlanWalker plw;
     if constexpr (PLAN) {
+      const long long W = a.plan_W;
+      long long chunk = (W + a.grid - 1) / a.grid;
+      if (chunk == 0) chunk = 1;
+      const long long r0 = (long long)cta * chunk;
       plw.segs = a.segs;
       plw.n_segs = a.n_segs;
       plw.B = B;
-      plw.s = (int)walk[0];
-      plw.r = r_begin;
-      plw.r1 = r_end;
+      plw.r = r0;
+      plw.r1 = r0 + chunk < W ? r0 + chunk : W;
+      plw.s = 0;
+      if (use_rec) {
+        reinterpret_cast<int32_t*>(rec_s)[lane] =
+            reinterpret_cast<const int32_t*>(a.starts + cta)[lane];
+        __syncwarp();
+      } else {
+        plw.s = r0 < W ? plan_find(a.segs, a.n_segs, r0) : a.n_segs;
+      }
     } else {
+      const WalkStart w = find_start(a.ctx, a.n_seq, B, H, a.max_blocks, a.grid, cta, a.status);
+      const long long r0 = (long long)cta * w.chunk;
       pw.ctx = a.ctx;
       pw.n_seq = a.n_seq;
       pw.B = B;
       pw.H = H;
       pw.max_blocks = a.max_blocks;
-      pw.s = (int)walk[0];
-      pw.pre = walk[1];
-      pw.r = r_begin;
-      pw.r1 = r_end;
+      pw.s = w.s;
+      pw.pre = w.pre;
+      pw.r = r0;
+      pw.r1 = r0 + w.chunk < w.W ? r0 + w.chunk : w.W;
     }
     bool rec_first = use_rec;  // the first piece comes from the start record
     auto next_piece = [&](Piece& p) -> bool {
@@ -394,10 +393,10 @@ __global__ void __launch_bounds__(kQ4Threads, kQ4CtasPerSm) decode_q4_kernel(con
         }
         const unsigned char* src = pool + (pool_row + static_cast<long long>(pid) * H + p.head) *
                                               static_cast<long long>(B * C::ROW);
-        const int slot = stage % NS;
-        unsigned char* dst = st + slot * C::SLOT_BYTES + (lane & 15) * unit_bytes;
-        if (stage >= NS && alive) {
-          if (!q4_wait(&empty[slot], ((stage / NS) & 1) ^ 1)) {
+        const int slot = stage % NST;
+        unsigned char* dst = st + slot * C::STAGE_BYTES + (lane & 15) * unit_bytes;
+        if (stage >= NST && alive) {
+          if (!q4_wait(&empty[slot], ((stage / NST) & 1) ^ 1)) {
             alive = false;
             if (lane == 0) record_status(a.status, 8);
           }
@@ -425,26 +424,31 @@ __global__ void __launch_bounds__(kQ4Threads, kQ4CtasPerSm) decode_q4_kernel(con
       p = pn;
       have = have_next;
     }
-    const int first = stage > NS ? stage - NS : 0;
+    const int first = stage > NST ? stage - NST : 0;
     for (int k = first; k < stage; ++k)
-      q4_wait(&full[k % NS], (k / NS) & 1);
+      q4_wait(&full[k % NST], (k / NST) & 1);
     return;
   }
 
   // -------------------------------------------------------------- consumers
+  reg_alloc<T::REGS_C>();
   wait_previous_grid();
   const int g = lane >> 2;  // groupID: row of A / C, column of B
   const int t = lane & 3;   // thread in group
   const uint32_t k_base = smem_u32(k_st);
-  const uint32_t v_base = smem_u32(v_st);
   const int cstride = PLAN ? a.c_max : G;  // columns per workspace slot
   bool alive = true;
-  int base = 0;  // slots before the piece
-  // q of this warp's column of a piece (column wn * 8 + g): dimensions
+  int slot = 0;        // stage being read
+  uint32_t phase = 0;  // and the parity of its full barrier
+  // n-tiles are dealt to the warps NTW at a time (a set); warps that share a set
+  // split its tokens.  q of this warp's column g of the set's tile j: dimensions
   // 32 q + 8 t .. + 7 of each group, raw bf16
-  auto load_q = [&](const Piece& pc, uint4 (&qr)[GR]) {
-    const int NTc = pc.ncols <= 8 ? 1 : (pc.ncols <= 16 ? 2 : 4);
-    const int col = (warp % NTc) * 8 + g;
+  auto n_sets = [&](const Piece& pc) {
+    const int nt = pc.ncols <= 8 ? 1 : (pc.ncols <= 16 ? 2 : 4);
+    return nt <= NTW ? 1 : nt / NTW;
+  };
+  auto load_q = [&](const Piece& pc, int j, uint4 (&qr)[GR]) {
+    const int col = ((warp % n_sets(pc)) * NTW + j) * 8 + g;
     const bool colv = col < pc.ncols;
     int seqm = pc.rep, gi = col;
     if constexpr (PLAN) {
@@ -458,26 +462,38 @@ __global__ void __launch_bounds__(kQ4Threads, kQ4CtasPerSm) decode_q4_kernel(con
 #pragma unroll
     for (int q = 0; q < GR; ++q) qr[q] = colv ? qw[q * 4 + t] : make_uint4(0u, 0u, 0u, 0u);
   };
-  // offsets inside a slot of what this lane reads of the first two tiles, and
-  // the step to the next two
-  auto unit_of = [](int r) -> uint32_t { return (r >> lur) * unit_bytes; };
-  auto row_of = [](int r) -> uint32_t { return r & (UR - 1); };
-  const int rk = (lane >> 4) * 16 + q4_srow(((lane >> 3) & 1) * 8 + (lane & 7));
-  const int rv = (lane >> 4) * 16 + q4_vrow(lane & 15);
-  const uint32_t at_kc = unit_of(rk) + row_of(rk) * 16, at_vc = unit_of(rv) + row_of(rv) * 16;
-  uint32_t at_ks[2], at_vs[2];  // scales of K rows g, g + 8 and of V's token pairs
+  // shared offset of token r's unit and its row inside the unit
+  auto unit_of = [&](int r) -> uint32_t { return (r >> lur) * unit_bytes; };
+  auto row_of = [&](int r) -> uint32_t { return r & (UR - 1); };
+  // offsets inside a stage of what this lane reads of the pass at token tb;
+  // those of a warp's first pass are kept (a narrow piece has no other)
+  struct Offsets {
+    int tb;
+    uint32_t kc, vc;        // K and V codes (lane's row of the matrix loads)
+    uint32_t ks[2], vs;     // scales of K rows g, g + 8 and of V's four tokens
+    uint32_t chk;           // V scales this lane checks: four tokens of a group
+  };
+  auto offsets = [&](int tb) -> Offsets {
+    Offsets x;
+    x.tb = tb;
+    const int rk = tb + (lane >> 4) * 16 + q4_srow(((lane >> 3) & 1) * 8 + (lane & 7));
+    const int rv = tb + (lane >> 4) * 16 + q4_vrow(lane & 15);
+    x.kc = unit_of(rk) + row_of(rk) * 16;
+    x.vc = unit_of(rv) + row_of(rv) * 16;
 #pragma unroll
-  for (int hi = 0; hi < 2; ++hi) {
-    const int r = q4_srow(g + 8 * hi);
-    at_ks[hi] = unit_of(r) + GR * UR * 16 + row_of(r) * GR * 2;
-    const int rp = q4_srow(2 * t + 8 * hi);  // even: a pair never crosses a unit
-    at_vs[hi] = unit_of(rp) + GR * UR * 16 + row_of(rp) * 2;
-  }
+    for (int hi = 0; hi < 2; ++hi) {
+      const int r = tb + q4_srow(g + 8 * hi);
+      x.ks[hi] = unit_of(r) + GR * UR * 16 + row_of(r) * GR * 2;
+    }
+    const int rp = tb + 4 * t;  // four tokens never cross a unit
+    x.vs = unit_of(rp) + GR * UR * 16 + row_of(rp) * 2;
+    const int rc = tb + 4 * (lane & 7);
+    x.chk = unit_of(rc) + GR * UR * 16 + ((lane >> 3) & (GR - 1)) * UR * 2 + row_of(rc) * 2;
+    return x;
+  };
+  // from a pass's first tile to its second
   constexpr uint32_t tile_ks = UR >= 32 ? 16u * GR * 2 : (16u >> lur) * unit_bytes;
   constexpr uint32_t tile_vs = UR >= 32 ? 16u * 2 : (16u >> lur) * unit_bytes;
-  constexpr uint32_t pair_c = UR >= 64 ? 32u * 16 : (32u >> lur) * unit_bytes;
-  constexpr uint32_t pair_ks = UR >= 64 ? 32u * GR * 2 : (32u >> lur) * unit_bytes;
-  constexpr uint32_t pair_vs = UR >= 64 ? 32u * 2 : (32u >> lur) * unit_bytes;
   int nread = 0;
   auto read_piece = [&](Piece& x) -> bool {
     const int di = nread % kPieceRing;
@@ -495,23 +511,27 @@ __global__ void __launch_bounds__(kQ4Threads, kQ4CtasPerSm) decode_q4_kernel(con
   };
   Piece p;
   while (read_piece(p)) {
-    uint4 qn[GR];
-    load_q(p, qn);
-    const int NT = p.ncols <= 8 ? 1 : (p.ncols <= 16 ? 2 : 4);  // n-tiles of the piece
-    const int WT = kQ4Warps / NT;                                 // warps per n-tile
-    const int wt = warp / NT;
+    uint4 qn[NTW][GR];
+#pragma unroll
+    for (int j = 0; j < NTW; ++j) load_q(p, j, qn[j]);
+    const int NP = n_sets(p);       // sets of n-tiles of the piece
+    const int WT = kQ4Warps / NP;   // warps per set
+    const int wt = warp / NP;
     // Q fragments.  Column g is scaled by the power of two that brings its
     // largest |q| into [2^14, 2^15): bf16's 8 bits then stay exact in fp16
-    // over 2^28 of range.  MMA 0 of a group takes dimensions 8t + {0, 4} and
-    // {2, 6}, MMA 1 (the nibbles times 16) 8t + {1, 5} and {3, 7} over 16.
-    uint32_t qf[GR][4];
-    uint32_t qoff;   // offset fragment, see below
-    float fcol[2];   // score factors of columns 2t and 2t + 1
-    {
+    // over 2^28 of range.  MMA 1 of a group takes whole bytes 16 n' + n (n' the
+    // odd dimension's nibble) with Q' / 16 as the factors, MMA 0 the low nibbles
+    // n with Q - Q' / 16, which takes the rest off again (rounded to fp16's 11
+    // bits, three more than q has).
+    uint32_t qf[NTW][GR][4];
+    uint32_t qoff[NTW];   // offset fragment, see below
+    float fcol[NTW][2];   // score factors of columns 2t and 2t + 1
+#pragma unroll
+    for (int j = 0; j < NTW; ++j) {
       uint32_t am = 0;
 #pragma unroll
       for (int q = 0; q < GR; ++q) {
-        const uint32_t w[4] = {qn[q].x, qn[q].y, qn[q].z, qn[q].w};
+        const uint32_t w[4] = {qn[j][q].x, qn[j][q].y, qn[j][q].z, qn[j][q].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           am = max(am, (w[i] << 16) & 0x7fffffffu);
@@ -525,26 +545,27 @@ __global__ void __launch_bounds__(kQ4Threads, kQ4CtasPerSm) decode_q4_kernel(con
       const float sc = __uint_as_float(static_cast<uint32_t>(268 - E) << 23);  // 2^(141 - E)
       // S = 2^24 * 2^(E - 141) * accumulator, times the score scale
       const float f = a.qscale * __uint_as_float(static_cast<uint32_t>(E) << 23) * 0x1p10f;
-      fcol[0] = __shfl_sync(0xffffffffu, f, 8 * t);
-      fcol[1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
+      fcol[j][0] = __shfl_sync(0xffffffffu, f, 8 * t);
+      fcol[j][1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
       float off[GR];
 #pragma unroll
       for (int q = 0; q < GR; ++q) {
-        const uint32_t w[4] = {qn[q].x, qn[q].y, qn[q].z, qn[q].w};
+        const uint32_t w[4] = {qn[j][q].x, qn[j][q].y, qn[j][q].z, qn[j][q].w};
+        uint32_t(&qx)[4] = qf[j][q];
         float x[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          x[2 * i] = __uint_as_float(w[i] << 16) * sc;
           x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u) * sc * 0.0625f;
+          x[2 * i] = __uint_as_float(w[i] << 16) * sc - x[2 * i + 1];
         }
-        qf[q][0] = pack_f16(x[0], x[4]);
-        qf[q][1] = pack_f16(x[2], x[6]);
-        qf[q][2] = pack_f16(x[1], x[5]);
-        qf[q][3] = pack_f16(x[3], x[7]);
-        // the offset's sum takes the values the MMAs take (as rounded)
-        float sum = (half_lo(qf[q][0]) + half_hi(qf[q][0])) + (half_lo(qf[q][1]) + half_hi(qf[q][1]));
-        sum += 16.f * ((half_lo(qf[q][2]) + half_hi(qf[q][2])) +
-                       (half_lo(qf[q][3]) + half_hi(qf[q][3])));
+        qx[0] = pack_f16(x[0], x[4]);
+        qx[1] = pack_f16(x[2], x[6]);
+        qx[2] = pack_f16(x[1], x[5]);
+        qx[3] = pack_f16(x[3], x[7]);
+        // the offset's sum, 8 Q0 + 136 Q1, takes the values the MMAs take (as
+        // rounded)
+        float sum = (half_lo(qx[0]) + half_hi(qx[0])) + (half_lo(qx[1]) + half_hi(qx[1]));
+        sum += 17.f * ((half_lo(qx[2]) + half_hi(qx[2])) + (half_lo(qx[3]) + half_hi(qx[3])));
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
         off[q] = sum * (-8.f * 0x1p-24f);  // below 1: |q| < 2^15
@@ -555,229 +576,295 @@ __global__ void __launch_bounds__(kQ4Threads, kQ4CtasPerSm) decode_q4_kernel(con
       // above
       const float u0 = GR == 4 && (t & 1) ? off[GR - 2] : (t & 1) ? 0.f : off[0];
       const float u1 = GR == 4 && (t & 1) ? off[GR - 1] : (t & 1) ? 0.f : off[1];
-      qoff = pack_f16(u0, u1);
-      if (t >= 2) qoff = pack_f16(u0 - half_lo(qoff), u1 - half_hi(qoff));
+      qoff[j] = pack_f16(u0, u1);
+      if (t >= 2) qoff[j] = pack_f16(u0 - half_lo(qoff[j]), u1 - half_hi(qoff[j]));
     }
-    float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
-    float o[C::MT][4];
+    Offsets at = offsets(wt * 32);
+    float m_run[NTW][2], l_run[NTW][2];
+    float e_run = kQ4Exp;  // weights are at most 2^e_run
+    float o[NTW][C::MT][4];
 #pragma unroll
-    for (int mt = 0; mt < C::MT; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
+    for (int j = 0; j < NTW; ++j) {
+      m_run[j][0] = m_run[j][1] = -INFINITY;
+      l_run[j][0] = l_run[j][1] = 0.f;
+#pragma unroll
+      for (int mt = 0; mt < C::MT; ++mt) o[j][mt][0] = o[j][mt][1] = o[j][mt][2] = o[j][mt][3] = 0.f;
+    }
+    // the offset's part of O (rows 0-7 times -8, rows 8-15 times -136), apart
+    // from it and added every few stages: summed apart over a long piece the two
+    // would cancel to a small rest of large sums (1.8x the error at 32,771
+    // tokens)
+    float ov[NTW][GR][4];
+    auto fold = [&]() {
+#pragma unroll
+      for (int j = 0; j < NTW; ++j)
+#pragma unroll
+        for (int q = 0; q < GR; ++q)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            o[j][2 * q][k] += ov[j][q][k];
+            o[j][2 * q + 1][k] += ov[j][q][k];
+            ov[j][q][k] = 0.f;
+          }
+    };
+#pragma unroll
+    for (int j = 0; j < NTW; ++j)
+#pragma unroll
+      for (int q = 0; q < GR; ++q) ov[j][q][0] = ov[j][q][1] = ov[j][q][2] = ov[j][q][3] = 0.f;
+    // the A operand of the offset's MMAs, kept in registers
+    uint32_t of[4];
+    asm volatile("mov.b32 %0, %4;\n\tmov.b32 %1, %5;\n\tmov.b32 %2, %4;\n\tmov.b32 %3, %5;"
+                 : "=r"(of[0]), "=r"(of[1]), "=r"(of[2]), "=r"(of[3])
+                 : "n"(kOffNib), "n"(kOffByte));
 
-    // slot r of the ring goes to the warps with wt = r mod WT (one per n-tile)
-    const int tok_first = p.b0 * B;
-    const int n_slots = (p.tok_end - tok_first + C::TS - 1) / C::TS;
-    for (int r = base + ((wt - base) & (WT - 1)); r < base + n_slots; r += WT) {
-      const int slot = r % NS;
-      if (alive && !q4_wait(&full[slot], (r / NS) & 1)) {
+    for (int tok0 = p.b0 * B; tok0 < p.tok_end; tok0 += C::TS) {
+      if (alive && !q4_wait(&full[slot], phase)) {
         alive = false;
         if (lane == 0) record_status(a.status, 8);
       }
       alive = __all_sync(0xffffffffu, alive);  // reconverge before ldmatrix / mma.sync
-      const int nv = min(p.tok_end - (tok_first + (r - base) * C::TS), C::TS);
-      const uint32_t kb = k_base + slot * C::SLOT_BYTES;
-      const uint32_t vb = v_base + slot * C::SLOT_BYTES;
-      // ---- S^T = K . Q^T, one accumulator per tile and group, weighted by
-      // its rows' K scales
-      float s[PT][4];
-#pragma unroll
-      for (int j = 0; j < PT / 2; ++j) {
-        uint32_t sc[2][2][GR / 2];  // scales of rows g and g + 8 of each tile
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          lds_scales<GR>(kb + at_ks[0] + j * pair_ks + i * tile_ks, sc[i][0]);
-          lds_scales<GR>(kb + at_ks[1] + j * pair_ks + i * tile_ks, sc[i][1]);
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          q4_mma_z(s[2 * j + i], GR == 4 && (t & 1) ? sc[i][0][GR / 2 - 1] : sc[i][0][0],
-                   GR == 4 && (t & 1) ? sc[i][1][GR / 2 - 1] : sc[i][1][0], 0u, 0u, qoff, 0u);
-#pragma unroll
-        for (int q = 0; q < GR; ++q) {
-          // ldmatrix: rows 0-7 and 8-15 of the first tile, then of the second
-          uint32_t w[4];
-          ldsm_x4(kb + at_kc + j * pair_c + q * UR * 16, w[0], w[1], w[2], w[3]);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t wa = w[2 * i], wb = w[2 * i + 1];
-            const uint32_t wa8 = wa >> 8, wb8 = wb >> 8;
-            float acc[4];
-            q4_mma_z(acc, wa & kNibLo, wb & kNibLo, wa8 & kNibLo, wb8 & kNibLo, qf[q][0],
-                     qf[q][1]);
-            q4_mma(acc, wa & kNibHi, wb & kNibHi, wa8 & kNibHi, wb8 & kNibHi, qf[q][2], qf[q][3]);
-            const float fl = q & 1 ? half_hi(sc[i][0][q / 2]) : half_lo(sc[i][0][q / 2]);
-            const float fh = q & 1 ? half_hi(sc[i][1][q / 2]) : half_lo(sc[i][1][q / 2]);
-            float(&x)[4] = s[2 * j + i];
-            x[0] = fmaf(fl, acc[0], x[0]);
-            x[1] = fmaf(fl, acc[1], x[1]);
-            x[2] = fmaf(fh, acc[2], x[2]);
-            x[3] = fmaf(fh, acc[3], x[3]);
-          }
-        }
-      }
-      // ---- mask: rows past the context, whatever their bytes hold
-      if (nv < C::TS) {
-#pragma unroll
-        for (int i = 0; i < PT; ++i) {
-          if (i * 16 + q4_srow(g) >= nv) s[i][0] = s[i][1] = -INFINITY;
-          if (i * 16 + q4_srow(g + 8) >= nv) s[i][2] = s[i][3] = -INFINITY;
-        }
-        // and their V scales zero (a NaN times a zero weight would reach the
-        // sum): every warp that reads the slot writes the same zeros, the fence
-        // orders them before the copy that refills it
-#pragma unroll
-        for (int r0 = 0; r0 < C::TS; r0 += 32) {
-          const int rr = r0 + lane;
-          if (rr >= nv) {
-            const uint32_t sa = vb + unit_of(rr) + GR * UR * 16 + row_of(rr) * 2;
+      const int nvalid = p.tok_end - tok0 < C::TS ? p.tok_end - tok0 : C::TS;
+      const uint32_t kb = k_base + slot * C::STAGE_BYTES;
+      const uint32_t vb = kb + NST * C::STAGE_BYTES;
+      // two 16-token tiles a pass: their chains of MMAs interleave, and one
+      // check of the running maximum covers both
+#pragma unroll 1
+      for (int tb = wt * 32; tb < nvalid; tb += WT * 32) {
+        const int nv = nvalid - tb;  // tokens of the pass inside the context (>= 1)
+        if (tb != at.tb) at = offsets(tb);
+        // past the context: V scales zero, whatever the bytes hold (a NaN times
+        // a zero weight would reach the sum).  This warp alone reads them, the
+        // fence orders the writes before the copy that refills the stage.
+        if (nv < 32) {
+          if (lane >= nv) {
+            const int r = tb + lane;
+            const uint32_t sa = vb + unit_of(r) + GR * UR * 16 + row_of(r) * 2;
 #pragma unroll
             for (int q = 0; q < GR; ++q)
               asm volatile("st.shared.b16 [%0], %1;" ::"r"(sa + q * UR * 2), "h"(
                                static_cast<uint16_t>(0))
                            : "memory");
           }
+          fence_async_smem();
+          __syncwarp();
         }
-        fence_async_smem();
-        __syncwarp();
-      }
-      // ---- reference of the weights, per column: p = 2^(s - m) with m the
-      // maximum at its last move plus kQ4Head, moved when a score passes it.
-      // So p <= 1 always (p times a scale stays inside fp16), the check is
-      // one vote, and moves are rare once the first tokens have set it.
-      float mx0 = -INFINITY, mx1 = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < PT; ++i) {
-        mx0 = fmaxf(mx0, fmaxf(s[i][0], s[i][2]));
-        mx1 = fmaxf(mx1, fmaxf(s[i][1], s[i][3]));
-      }
-      mx0 *= fcol[0];
-      mx1 *= fcol[1];
-      if (__any_sync(0xffffffffu, (mx0 > m_run[0]) | (mx1 > m_run[1]))) {
-        float n0 = mx0, n1 = mx1;
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1) {
-          n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, off));
-          n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, off));
-        }
-        n0 = n0 > m_run[0] ? n0 + kQ4Head : m_run[0];
-        n1 = n1 > m_run[1] ? n1 + kQ4Head : m_run[1];
-        const float al0 = exp2_approx(m_run[0] - n0), al1 = exp2_approx(m_run[1] - n1);
-        m_run[0] = n0;
-        m_run[1] = n1;
-        l_run[0] *= al0;
-        l_run[1] *= al1;
-#pragma unroll
-        for (int mt = 0; mt < C::MT; ++mt) {
-          o[mt][0] *= al0;
-          o[mt][1] *= al1;
-          o[mt][2] *= al0;
-          o[mt][3] *= al1;
-        }
-      }
-      // ---- P^T in fp16 (11 bits), transposed: b[i][0] holds tokens
-      // srow(2t), srow(2t + 1) of column g, b[i][1] srow(2t + 8), + 1
-      uint32_t b[PT][2];
-#pragma unroll
-      for (int i = 0; i < PT; ++i) {
-        const float p0 = exp2_approx(fmaf(s[i][0], fcol[0], -m_run[0]));
-        const float p1 = exp2_approx(fmaf(s[i][1], fcol[1], -m_run[1]));
-        const float p2 = exp2_approx(fmaf(s[i][2], fcol[0], -m_run[0]));
-        const float p3 = exp2_approx(fmaf(s[i][3], fcol[1], -m_run[1]));
-        l_run[0] += p0 + p2;
-        l_run[1] += p1 + p3;
-        b[i][0] = q4_movm(pack_f16(p0, p1));
-        b[i][1] = q4_movm(pack_f16(p2, p3));
-      }
-      // ---- O^T += V^T . (P vs)^T per group.  The V scales of a token pair
-      // are adjacent, so P' is one fp16 product per register (a second
-      // rounding to 11 bits; p <= 1 and the scale is a finite fp16, so it
-      // never overflows).
-#pragma unroll
-      for (int j = 0; j < PT / 2; ++j) {
-#pragma unroll
-        for (int q = 0; q < GR; ++q) {
-          uint32_t w[4];
-          ldsm8_x2_t(vb + at_vc + j * pair_c + q * UR * 16, w[0], w[1], w[2], w[3]);
+        const uint2 chk = lds64(vb + at.chk);
+        // ---- S^T = K . Q^T per tile: one accumulator per group, weighted by
+        // its rows' K scales
+        float s[NTW][2][4];
+        {
+          // ldmatrix: rows 0-7 and 8-15 of the first tile, then of the second
+          const uint32_t ka = kb + at.kc;
+          uint32_t sc[2][2][GR / 2];  // scales of rows g and g + 8 of each tile
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const uint32_t sa = vb + j * pair_vs + i * tile_vs + q * UR * 2;
-            const uint32_t c0 = hmul2(b[2 * j + i][0], lds32(sa + at_vs[0]));
-            const uint32_t c1 = hmul2(b[2 * j + i][1], lds32(sa + at_vs[1]));
-            const uint32_t r0 = w[2 * i], r1 = w[2 * i + 1], r08 = r0 >> 8, r18 = r1 >> 8;
-            q4_mma(o[2 * q], r0 & kNibLo, r0 & kNibHi, r08 & kNibLo, r08 & kNibHi, c0, c1);
-            q4_mma(o[2 * q + 1], r1 & kNibLo, r1 & kNibHi, r18 & kNibLo, r18 & kNibHi, c0, c1);
-            q4_mma(o[2 * q], kNibOffLo, kNibOffHi, kNibOffLo, kNibOffHi, c0, c1);
-            q4_mma(o[2 * q + 1], kNibOffLo, kNibOffHi, kNibOffLo, kNibOffHi, c0, c1);
+            lds_scales<GR>(kb + at.ks[0] + i * tile_ks, sc[i][0]);
+            lds_scales<GR>(kb + at.ks[1] + i * tile_ks, sc[i][1]);
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < NTW; ++j)
+              q4_mma_z(s[j][i], GR == 4 && (t & 1) ? sc[i][0][GR / 2 - 1] : sc[i][0][0],
+                       GR == 4 && (t & 1) ? sc[i][1][GR / 2 - 1] : sc[i][1][0], 0u, 0u, qoff[j],
+                       0u);
+#pragma unroll
+          for (int q = 0; q < GR; ++q) {
+            uint32_t w[4];
+            ldsm_x4(ka + q * UR * 16, w[0], w[1], w[2], w[3]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t wa = w[2 * i], wb = w[2 * i + 1];
+              const uint32_t wa8 = q4_odd_bytes(wa), wb8 = q4_odd_bytes(wb);
+              const float fl = q & 1 ? half_hi(sc[i][0][q / 2]) : half_lo(sc[i][0][q / 2]);
+              const float fh = q & 1 ? half_hi(sc[i][1][q / 2]) : half_lo(sc[i][1][q / 2]);
+#pragma unroll
+              for (int j = 0; j < NTW; ++j) {
+                float acc[4];
+                q4_mma_z(acc, wa & kNibLo, wb & kNibLo, wa8 & kNibLo, wb8 & kNibLo, qf[j][q][0],
+                         qf[j][q][1]);
+                q4_mma(acc, wa & kByte, wb & kByte, wa8, wb8, qf[j][q][2], qf[j][q][3]);
+                s[j][i][0] = fmaf(fl, acc[0], s[j][i][0]);
+                s[j][i][1] = fmaf(fl, acc[1], s[j][i][1]);
+                s[j][i][2] = fmaf(fh, acc[2], s[j][i][2]);
+                s[j][i][3] = fmaf(fh, acc[3], s[j][i][3]);
+              }
+            }
+          }
+        }
+        if (nv < 32) {  // rows past the context
+#pragma unroll
+          for (int j = 0; j < NTW; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (i * 16 + q4_srow(g) >= nv) s[j][i][0] = s[j][i][1] = -INFINITY;
+              if (i * 16 + q4_srow(g + 8) >= nv) s[j][i][2] = s[j][i][3] = -INFINITY;
+            }
+        }
+        // ---- reference of the weights, per column: p = 2^(s - m), m the
+        // maximum at its last move plus kQ4Head less e_run, moved when a score
+        // passes m + e_run or e_run changes.  So p <= 2^e_run always, the check
+        // is one vote, and moves are rare once the first tokens have set it.
+        float mx[NTW][2];
+        const bool big = ((chk.x | chk.y) & 0x40004000u) != 0 && e_run > 0.f;
+        bool move = big;
+#pragma unroll
+        for (int j = 0; j < NTW; ++j)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            mx[j][k] = fmaxf(fmaxf(s[j][0][k], s[j][0][2 + k]), fmaxf(s[j][1][k], s[j][1][2 + k])) *
+                       fcol[j][k];
+            move |= mx[j][k] > m_run[j][k] + e_run;
+          }
+        if (__any_sync(0xffffffffu, move)) {
+          const float e_old = e_run;
+          if (__any_sync(0xffffffffu, big)) e_run = 0.f;
+          fold();
+#pragma unroll
+          for (int j = 0; j < NTW; ++j)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              float n = mx[j][k];
+#pragma unroll
+              for (int off = 4; off < 32; off <<= 1)
+                n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, off));
+              n = (n > m_run[j][k] + e_old ? n + kQ4Head : m_run[j][k] + e_old) - e_run;
+              const float al = exp2_approx(m_run[j][k] - n);
+              m_run[j][k] = n;
+              l_run[j][k] *= al;
+#pragma unroll
+              for (int mt = 0; mt < C::MT; ++mt) {
+                o[j][mt][k] *= al;
+                o[j][mt][2 + k] *= al;
+              }
+            }
+        }
+        // ---- P^T in fp16 (11 bits), transposed: b[.][i][0] holds tokens
+        // srow(2t), srow(2t + 1) of column g, b[.][i][1] srow(2t + 8), + 1
+        uint32_t b[NTW][2][2];
+#pragma unroll
+        for (int j = 0; j < NTW; ++j)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float p0 = exp2_approx(fmaf(s[j][i][0], fcol[j][0], -m_run[j][0]));
+            const float p1 = exp2_approx(fmaf(s[j][i][1], fcol[j][1], -m_run[j][1]));
+            const float p2 = exp2_approx(fmaf(s[j][i][2], fcol[j][0], -m_run[j][0]));
+            const float p3 = exp2_approx(fmaf(s[j][i][3], fcol[j][1], -m_run[j][1]));
+            l_run[j][0] += p0 + p2;
+            l_run[j][1] += p1 + p3;
+            b[j][i][0] = q4_movm(pack_f16(p0, p1));
+            b[j][i][1] = q4_movm(pack_f16(p2, p3));
+          }
+        // ---- O^T += V^T . (P vs)^T per group.  The V scales of a lane's four
+        // tokens are adjacent, so P' is one fp16 product per register (a second
+        // rounding to 11 bits; p times a scale stays inside fp16).  Row g of a
+        // tile takes the low nibbles, row g + 8 the whole bytes 16 n' + n: four
+        // operations a word of eight nibbles, and the low ones are taken off
+        // again at the end.
+        {
+          const uint32_t va = vb + at.vc;
+#pragma unroll
+          for (int q = 0; q < GR; ++q) {
+            uint32_t w[4];
+            ldsm8_x2_t(va + q * UR * 16, w[0], w[1], w[2], w[3]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint2 sv = lds64(vb + at.vs + i * tile_vs + q * UR * 2);
+              const uint32_t r0 = w[2 * i], r1 = w[2 * i + 1];
+              const uint32_t r08 = q4_odd_bytes(r0), r18 = q4_odd_bytes(r1);
+#pragma unroll
+              for (int j = 0; j < NTW; ++j) {
+                const uint32_t c0 = hmul2(b[j][i][0], sv.x), c1 = hmul2(b[j][i][1], sv.y);
+                q4_mma(o[j][2 * q], r0 & kNibLo, r0 & kByte, r08 & kNibLo, r08, c0, c1);
+                q4_mma(o[j][2 * q + 1], r1 & kNibLo, r1 & kByte, r18 & kNibLo, r18, c0, c1);
+                q4_mma(ov[j][q], of[0], of[1], of[2], of[3], c0, c1);
+              }
+            }
           }
         }
       }
+      if ((tok0 / C::TS & 7) == 7) fold();
       __syncwarp();
-      if (lane == 0) mbar_arrive_n(&empty[slot], WT);  // WT x NT = kQ4Warps
+      if (lane == 0) mbar_arrive(&empty[slot]);
+      if (++slot == NST) {
+        slot = 0;
+        phase ^= 1;
+      }
     }
-    base += n_slots;
-    // row g of m-tile 2q + h is dimension 32 q + 16 h + 2 g, row g + 8 the next
-    // one (nibbles times 16)
+    // row g of m-tile 2q + h is dimension 32 q + 16 h + 2 g, row g + 8, less
+    // row g, the next one times 16
+    fold();
 #pragma unroll
-    for (int mt = 0; mt < C::MT; ++mt)
+    for (int j = 0; j < NTW; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        o[mt][i] *= i < 2 ? 0x1p24f : 0x1p20f;
+      for (int mt = 0; mt < C::MT; ++mt)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          o[j][mt][2 + k] = (o[j][mt][2 + k] - o[j][mt][k]) * 0x1p20f;
+          o[j][mt][k] *= 0x1p24f;
+        }
 
-    // ---- combine the states of the warps that share an n-tile
+    // ---- combine the states of the warps that share a set
 #pragma unroll
-    for (int off = 4; off < 32; off <<= 1) {
-      l_run[0] += __shfl_xor_sync(0xffffffffu, l_run[0], off);
-      l_run[1] += __shfl_xor_sync(0xffffffffu, l_run[1], off);
-    }
-    if (g == 0) {
+    for (int j = 0; j < NTW; ++j)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        cmb_ml[(warp * 8 + 2 * t + k) * 2] = m_run[k];
-        cmb_ml[(warp * 8 + 2 * t + k) * 2 + 1] = l_run[k];
-      }
-    }
-    const long long slot_id = (long long)blockIdx.x + p.seg;
-    for (int pc = 0; pc < 8; pc += C::CC) {
-      if (pc >= p.ncols) break;  // no column of any n-tile in this pass
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int c8 = 2 * t + k;
-        if (c8 >= pc && c8 < pc + C::CC) {
+        for (int off = 4; off < 32; off <<= 1)
+          l_run[j][k] += __shfl_xor_sync(0xffffffffu, l_run[j][k], off);
+        if (g == 0) {
+          cmb_ml[((warp * NTW + j) * 8 + 2 * t + k) * 2] = m_run[j][k];
+          cmb_ml[((warp * NTW + j) * 8 + 2 * t + k) * 2 + 1] = l_run[j][k];
+        }
+      }
+    const long long slot_id = (long long)cta + p.seg;
 #pragma unroll
-          for (int mt = 0; mt < C::MT; ++mt)
-            *reinterpret_cast<float2*>(&cmb_o[(warp * C::CC + c8 - pc) * D + mt * 16 + 2 * g]) =
-                make_float2(o[mt][k], o[mt][2 + k]);
+    for (int j = 0; j < NTW; ++j) {
+      for (int pc = 0; pc < 8; pc += C::CC) {
+        if (j * 8 + pc >= p.ncols) break;  // no column of any set in this pass
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int c8 = 2 * t + k;
+          if (c8 >= pc && c8 < pc + C::CC) {
+#pragma unroll
+            for (int mt = 0; mt < C::MT; ++mt)
+              *reinterpret_cast<float2*>(&cmb_o[(warp * C::CC + c8 - pc) * D + mt * 16 + 2 * g]) =
+                  make_float2(o[j][mt][k], o[j][mt][2 + k]);
+          }
         }
+        named_bar_sync(1 + team, kQ4Warps * 32);
+        constexpr int D4 = D / 4;
+        for (int idx = threadIdx.x & (kQ4Warps * 32 - 1); idx < NP * C::CC * D4;
+             idx += kQ4Warps * 32) {
+          const int set = idx / (C::CC * D4);
+          const int rem = idx - set * C::CC * D4;
+          const int cc = rem / D4, d = (rem - cc * D4) * 4;
+          const int col = (set * NTW + j) * 8 + pc + cc;
+          if (col >= p.ncols) continue;
+          float M = -INFINITY;
+          for (int i = 0; i < WT; ++i)
+            M = fmaxf(M, cmb_ml[(((set + i * NP) * NTW + j) * 8 + pc + cc) * 2]);
+          float L = 0.f;
+          float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int i = 0; i < WT; ++i) {
+            const int w = set + i * NP;
+            const float* ml = &cmb_ml[((w * NTW + j) * 8 + pc + cc) * 2];
+            const float f = ml[0] == -INFINITY ? 0.f : exp2_approx(ml[0] - M);
+            L += f * ml[1];
+            const float4 v = *reinterpret_cast<const float4*>(&cmb_o[(w * C::CC + cc) * D + d]);
+            O.x += f * v.x;
+            O.y += f * v.y;
+            O.z += f * v.z;
+            O.w += f * v.w;
+          }
+          *reinterpret_cast<float4*>(&a.ws_o[(slot_id * cstride + col) * D + d]) = O;
+          if (d == 0) {
+            a.ws_ml[(slot_id * cstride + col) * 2] = M;
+            a.ws_ml[(slot_id * cstride + col) * 2 + 1] = L;
+          }
+        }
+        named_bar_sync(1 + team, kQ4Warps * 32);
       }
-      named_bar_sync(1, kQ4Warps * 32);
-      constexpr int D4 = D / 4;
-      for (int idx = threadIdx.x; idx < NT * C::CC * D4; idx += kQ4Warps * 32) {
-        const int wni = idx / (C::CC * D4);
-        const int rem = idx - wni * C::CC * D4;
-        const int cc = rem / D4, d = (rem - cc * D4) * 4;
-        const int col = wni * 8 + pc + cc;
-        if (col >= p.ncols) continue;
-        float M = -INFINITY;
-        for (int j = 0; j < WT; ++j) M = fmaxf(M, cmb_ml[((wni + j * NT) * 8 + pc + cc) * 2]);
-        float L = 0.f;
-        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int j = 0; j < WT; ++j) {
-          const int w = wni + j * NT;
-          const float mw = cmb_ml[(w * 8 + pc + cc) * 2];
-          const float f = mw == -INFINITY ? 0.f : exp2_approx(mw - M);
-          L += f * cmb_ml[(w * 8 + pc + cc) * 2 + 1];
-          const float4 v = *reinterpret_cast<const float4*>(&cmb_o[(w * C::CC + cc) * D + d]);
-          O.x += f * v.x;
-          O.y += f * v.y;
-          O.z += f * v.z;
-          O.w += f * v.w;
-        }
-        *reinterpret_cast<float4*>(&a.ws_o[(slot_id * cstride + col) * D + d]) = O;
-        if (d == 0) {
-          a.ws_ml[(slot_id * cstride + col) * 2] = M;
-          a.ws_ml[(slot_id * cstride + col) * 2 + 1] = L;
-        }
-      }
-      named_bar_sync(1, kQ4Warps * 32);
     }
   }
 }

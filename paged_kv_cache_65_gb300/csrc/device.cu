@@ -78,7 +78,8 @@ enum DecodeKernel { kKernelCudaCores, kKernelMma, kKernelTc };
 
 DecodeKernel decode_kernel(const kvPool* p) {
   const bool mma = p->mma_ok;
-  const bool tc = p->mma_ok && pool_tc_decode_shape(p);
+  // a q4_0 pool's wide form serves plans only
+  const bool tc = p->mma_ok && pool_tc_decode_shape(p) && p->dtype != KV_DTYPE_Q4_0;
   switch (p->decode_path) {
     case 1: return kKernelCudaCores;
     case 2: return mma ? kKernelMma : kKernelCudaCores;
@@ -936,14 +937,9 @@ kvStatus paged_decode_partials(kvPool* p, int layer, const void* d_q, int n_q_he
   cudaError_t e;
   if (p->dtype == KV_DTYPE_Q4_0) {
     if (kern == kKernelCudaCores) return KV_ERR_UNSUPPORTED;  // no CUDA-core pass over codes
-    if (kern == kKernelTc) {
-      e = pkv::launch_decode_q4_tc(a, p->sm_count, kMaxDecodeCtas, grid_io, as_stream(stream),
-                                   p->pdl);
-      supported = true;
-    } else {
-      e = pkv::launch_decode_q4(p->D, a, p->sm_count, kMaxDecodeCtas, grid_io, as_stream(stream),
-                                p->pdl, &supported);
-    }
+    // at most eight columns without a plan
+    e = pkv::launch_decode_q4(p->D, a, false, p->sm_count, kMaxDecodeCtas, grid_io,
+                              as_stream(stream), p->pdl, &supported);
   } else if (p->dtype == KV_DTYPE_FP8_E4M3 && kern == kKernelTc) {
     const CUtensorMap& tk = *reinterpret_cast<const CUtensorMap*>(p->tmap[2]);
     const CUtensorMap& tv = *reinterpret_cast<const CUtensorMap*>(p->tmap[3]);
@@ -1122,18 +1118,15 @@ kvStatus partials_planned(kvPool* p, int layer, const void* d_q, int n_q_heads,
   const CUtensorMap& tv = *reinterpret_cast<const CUtensorMap*>(p->tmap[3]);
   bool supported = true;
   const cudaError_t e =
-      tc ? (p->dtype == KV_DTYPE_Q4_0
-                ? pkv::launch_decode_q4_tc(a, p->sm_count, kMaxDecodeCtas, &p->grid_tc,
-                                           as_stream(stream), p->pdl)
-            : p->dtype == KV_DTYPE_FP8_E4M3
+      p->dtype == KV_DTYPE_Q4_0
+          ? pkv::launch_decode_q4(p->D, a, tc, p->sm_count, kMaxDecodeCtas,
+                                  tc ? &p->grid_tc : &p->grid_by_g[ilog2_small(G)],
+                                  as_stream(stream), p->pdl, &supported)
+      : tc ? (p->dtype == KV_DTYPE_FP8_E4M3
                 ? pkv::launch_tc_fp8(tk, tv, a, p->sm_count, kMaxDecodeCtas, &p->grid_tc,
                                      as_stream(stream), pdl)
                 : pkv::launch_tc_bf16(tk, tv, a, p->sm_count, kMaxDecodeCtas, &p->grid_tc,
                                       as_stream(stream), pdl))
-      : p->dtype == KV_DTYPE_Q4_0
-          ? pkv::launch_decode_q4(p->D, a, p->sm_count, kMaxDecodeCtas,
-                                  &p->grid_by_g[ilog2_small(G)], as_stream(stream), p->pdl,
-                                  &supported)
       : p->dtype == KV_DTYPE_Q8_0
           ? pkv::launch_mma_q8(p->D, G, tk, tv, a, p->sm_count, kMaxDecodeCtas,
                                &p->grid_by_g[ilog2_small(G)], as_stream(stream), pdl,

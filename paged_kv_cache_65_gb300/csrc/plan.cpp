@@ -406,7 +406,7 @@ kvStatus plan_build(const kvPool* p, const int32_t* seq_ids, int n_seq, int n_q_
       int64_t wide = 0, all = 0;
       for (const PlanSeg& s : segs) {
         all += s.b1 - s.b0;
-        if (s.ncols > 16) wide += s.b1 - s.b0;
+        if (s.ncols > (p->dtype == KV_DTYPE_Q4_0 ? 8 : 16)) wide += s.b1 - s.b0;
       }
       if (all > 0 && 2 * wide >= all) kernel = kPlanKernelTc;
     }

@@ -133,10 +133,11 @@ inline bool pool_tc_shape(const kvPool* p) {
 
 // The tcgen05 decode pass: bfloat16 as above, or FP8 codes with D_h = 128
 // (converted to fp16 in the pass: K rows into tensor memory, V rows into
-// shared memory), or q4_0 with D_h = 128 (the same way).
+// shared memory).  A q4_0 pool has the wide form of its warp-level pass in its
+// place.
 inline bool pool_tc_decode_shape(const kvPool* p) {
-  return (p->dtype == KV_DTYPE_BF16 || p->dtype == KV_DTYPE_FP8_E4M3 ||
-          p->dtype == KV_DTYPE_Q4_0) &&
+  if (p->dtype == KV_DTYPE_Q4_0) return pool_tensor_core_shape(p);
+  return (p->dtype == KV_DTYPE_BF16 || p->dtype == KV_DTYPE_FP8_E4M3) &&
          pool_tensor_core_shape(p) && p->D == 128;
 }
 
