@@ -113,6 +113,14 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   return r;
 }
 
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 r;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "r"(addr));
+  return r;
+}
+
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   uint32_t r;
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(addr));
@@ -193,6 +201,7 @@ constexpr int decode_q4_team_bytes() {
   constexpr int n = 2 * T::NST * C::STAGE_BYTES       // K and V stages
                     + kQ4Warps * C::CC * D * 4        // combine: O per warp, CC columns at a time
                     + kQ4Warps * T::NTW * 8 * 2 * 4   // combine: m, l per warp and column
+                    + (WIDE ? 2 * T::NTW * C::GR * 512 : 0)  // Q fragments of two sets
                     + 2 * T::NST * 8                  // mbarriers
                     + kTableCache * 4                 // producer table cache
                     + kPieceRing * (48 + 16)          // piece descriptors and their mbarriers
@@ -217,7 +226,8 @@ __global__ void __launch_bounds__(Q4Team<WIDE>::THREADS, 1) decode_q4_kernel(con
   unsigned char* v_st = k_st + NST * C::STAGE_BYTES;
   float* cmb_o = reinterpret_cast<float*>(v_st + NST * C::STAGE_BYTES);
   float* cmb_ml = cmb_o + kQ4Warps * C::CC * D;
-  uint64_t* full = reinterpret_cast<uint64_t*>(cmb_ml + kQ4Warps * NTW * 8 * 2);
+  uint4* q_frag = reinterpret_cast<uint4*>(cmb_ml + kQ4Warps * NTW * 8 * 2);
+  uint64_t* full = reinterpret_cast<uint64_t*>(q_frag + (WIDE ? 2 * NTW * GR * 32 : 0));
   uint64_t* empty = full + NST;
   uint64_t* dfull = empty + NST;
   uint64_t* dempty = dfull + kPieceRing;
@@ -580,6 +590,20 @@ __global__ void __launch_bounds__(Q4Team<WIDE>::THREADS, 1) decode_q4_kernel(con
       if (t >= 2) qoff[j] = pack_f16(u0 - half_lo(qoff[j]), u1 - half_hi(qoff[j]));
     }
     Offsets at = offsets(wt * 32);
+    // WIDE: the fragments go through shared memory, which leaves the registers to
+    // O; the warps of a set hold the same ones
+    const uint32_t q_addr = smem_u32(q_frag) + ((warp % NP) * NTW * GR * 32 + lane) * 16;
+    if constexpr (WIDE) {
+      if (wt == 0) {
+#pragma unroll
+        for (int j = 0; j < NTW; ++j)
+#pragma unroll
+          for (int q = 0; q < GR; ++q)
+            q_frag[((warp % NP) * NTW * GR + j * GR + q) * 32 + lane] =
+                make_uint4(qf[j][q][0], qf[j][q][1], qf[j][q][2], qf[j][q][3]);
+      }
+      named_bar_sync(1 + team, kQ4Warps * 32);
+    }
     float m_run[NTW][2], l_run[NTW][2];
     float e_run = kQ4Exp;  // weights are at most 2^e_run
     float o[NTW][C::MT][4];
@@ -672,6 +696,11 @@ __global__ void __launch_bounds__(Q4Team<WIDE>::THREADS, 1) decode_q4_kernel(con
           for (int q = 0; q < GR; ++q) {
             uint32_t w[4];
             ldsm_x4(ka + q * UR * 16, w[0], w[1], w[2], w[3]);
+            uint4 fq[NTW];
+#pragma unroll
+            for (int j = 0; j < NTW; ++j)
+              fq[j] = WIDE ? lds128(q_addr + (j * GR + q) * 512)
+                           : make_uint4(qf[j][q][0], qf[j][q][1], qf[j][q][2], qf[j][q][3]);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const uint32_t wa = w[2 * i], wb = w[2 * i + 1];
@@ -681,9 +710,9 @@ __global__ void __launch_bounds__(Q4Team<WIDE>::THREADS, 1) decode_q4_kernel(con
 #pragma unroll
               for (int j = 0; j < NTW; ++j) {
                 float acc[4];
-                q4_mma_z(acc, wa & kNibLo, wb & kNibLo, wa8 & kNibLo, wb8 & kNibLo, qf[j][q][0],
-                         qf[j][q][1]);
-                q4_mma(acc, wa & kByte, wb & kByte, wa8, wb8, qf[j][q][2], qf[j][q][3]);
+                q4_mma_z(acc, wa & kNibLo, wb & kNibLo, wa8 & kNibLo, wb8 & kNibLo, fq[j].x,
+                         fq[j].y);
+                q4_mma(acc, wa & kByte, wb & kByte, wa8, wb8, fq[j].z, fq[j].w);
                 s[j][i][0] = fmaf(fl, acc[0], s[j][i][0]);
                 s[j][i][1] = fmaf(fl, acc[1], s[j][i][1]);
                 s[j][i][2] = fmaf(fh, acc[2], s[j][i][2]);
