@@ -90,8 +90,6 @@ __device__ __forceinline__ int q4_vrow(int i) { return (i & ~3) + 2 * (i & 1) + 
 
 constexpr uint32_t kNibLo = 0x000f000fu;  // n * 2^-24
 constexpr uint32_t kByte = 0x00ff00ffu;   // (16 n' + n) * 2^-24, n' the high nibble
-constexpr uint32_t kOffNib = 0x80088008u;   // -8 * 2^-24 twice
-constexpr uint32_t kOffByte = 0x80888088u;  // -136 * 2^-24 twice
 
 // Headroom of a column's largest weight over the maximum that set it, in
 // base-2 units: the weights of a moved maximum are 2^(e - kQ4Head), e below.
@@ -136,6 +134,15 @@ __device__ __forceinline__ void q4_mma(float (&d)[4], uint32_t a0, uint32_t a1, 
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// D += A . B for an A whose rows 8 .. 15 are zero: the upper half of D is not kept.
+__device__ __forceinline__ void q4_mma_rows8(float (&d)[2], uint32_t a0, uint32_t a2, uint32_t b0,
+                                             uint32_t b1) {
+  float z0, z1;
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%5}, "
+      "{%7,%8}, {%0,%1,%9,%9};"
+      : "+f"(d[0]), "+f"(d[1]), "=f"(z0), "=f"(z1)
+      : "r"(a0), "r"(0u), "r"(a2), "r"(b0), "r"(b1), "f"(0.f));
 }
 // Bytes 1 and 3 of a word as halves: the fp16 operands 16 n' + n of them.
 __device__ __forceinline__ uint32_t q4_odd_bytes(uint32_t w) { return __byte_perm(w, 0, 0x4341); }
@@ -481,6 +488,7 @@ __global__ void __launch_bounds__(Q4Team<WIDE>::THREADS, 1) decode_q4_kernel(con
     int tb;
     uint32_t kc, vc;        // K and V codes (lane's row of the matrix loads)
     uint32_t ks[2], vs;     // scales of K rows g, g + 8 and of V's four tokens
+    uint32_t vo;            // V scales of group g & 3 (rows of the offset's MMA)
     uint32_t chk;           // V scales this lane checks: four tokens of a group
   };
   auto offsets = [&](int tb) -> Offsets {
@@ -497,6 +505,7 @@ __global__ void __launch_bounds__(Q4Team<WIDE>::THREADS, 1) decode_q4_kernel(con
     }
     const int rp = tb + 4 * t;  // four tokens never cross a unit
     x.vs = unit_of(rp) + GR * UR * 16 + row_of(rp) * 2;
+    x.vo = x.vs + (g & (GR - 1)) * UR * 2;
     const int rc = tb + 4 * (lane & 7);
     x.chk = unit_of(rc) + GR * UR * 16 + ((lane >> 3) & (GR - 1)) * UR * 2 + row_of(rc) * 2;
     return x;
@@ -614,32 +623,30 @@ __global__ void __launch_bounds__(Q4Team<WIDE>::THREADS, 1) decode_q4_kernel(con
 #pragma unroll
       for (int mt = 0; mt < C::MT; ++mt) o[j][mt][0] = o[j][mt][1] = o[j][mt][2] = o[j][mt][3] = 0.f;
     }
-    // the offset's part of O (rows 0-7 times -8, rows 8-15 times -136), apart
-    // from it and added every few stages: summed apart over a long piece the two
-    // would cancel to a small rest of large sums (1.8x the error at 32,771
-    // tokens)
-    float ov[NTW][GR][4];
+    // The offset's part of O, -8 sum_t vs[t][q] p[t], is the same for every
+    // dimension of a group: an MMA with the V scales as its rows, one for all
+    // groups (row q; those past the groups repeat them).  It is kept apart from O
+    // and added every few stages: summed apart over a long piece the two would
+    // cancel to a small rest of large sums (1.8x the error at 32,771 tokens).
+    float ov[NTW][2];
+#pragma unroll
+    for (int j = 0; j < NTW; ++j) ov[j][0] = ov[j][1] = 0.f;
     auto fold = [&]() {
 #pragma unroll
       for (int j = 0; j < NTW; ++j)
 #pragma unroll
-        for (int q = 0; q < GR; ++q)
+        for (int k = 0; k < 2; ++k) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            o[j][2 * q][k] += ov[j][q][k];
-            o[j][2 * q + 1][k] += ov[j][q][k];
-            ov[j][q][k] = 0.f;
+          for (int q = 0; q < GR; ++q) {
+            const float x = __shfl_sync(0xffffffffu, ov[j][k], 4 * q + t);
+            o[j][2 * q][k] = fmaf(x, -8.f * 0x1p-24f, o[j][2 * q][k]);
+            o[j][2 * q + 1][k] = fmaf(x, -8.f * 0x1p-24f, o[j][2 * q + 1][k]);
+            o[j][2 * q][2 + k] = fmaf(x, -136.f * 0x1p-24f, o[j][2 * q][2 + k]);
+            o[j][2 * q + 1][2 + k] = fmaf(x, -136.f * 0x1p-24f, o[j][2 * q + 1][2 + k]);
           }
+          ov[j][k] = 0.f;
+        }
     };
-#pragma unroll
-    for (int j = 0; j < NTW; ++j)
-#pragma unroll
-      for (int q = 0; q < GR; ++q) ov[j][q][0] = ov[j][q][1] = ov[j][q][2] = ov[j][q][3] = 0.f;
-    // the A operand of the offset's MMAs, kept in registers
-    uint32_t of[4];
-    asm volatile("mov.b32 %0, %4;\n\tmov.b32 %1, %5;\n\tmov.b32 %2, %4;\n\tmov.b32 %3, %5;"
-                 : "=r"(of[0]), "=r"(of[1]), "=r"(of[2]), "=r"(of[3])
-                 : "n"(kOffNib), "n"(kOffByte));
 
     for (int tok0 = p.b0 * B; tok0 < p.tok_end; tok0 += C::TS) {
       if (alive && !q4_wait(&full[slot], phase)) {
@@ -793,6 +800,12 @@ __global__ void __launch_bounds__(Q4Team<WIDE>::THREADS, 1) decode_q4_kernel(con
         {
           const uint32_t va = vb + at.vc;
 #pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint2 so = lds64(vb + at.vo + i * tile_vs);
+#pragma unroll
+            for (int j = 0; j < NTW; ++j) q4_mma_rows8(ov[j], so.x, so.y, b[j][i][0], b[j][i][1]);
+          }
+#pragma unroll
           for (int q = 0; q < GR; ++q) {
             uint32_t w[4];
             ldsm8_x2_t(va + q * UR * 16, w[0], w[1], w[2], w[3]);
@@ -806,7 +819,6 @@ __global__ void __launch_bounds__(Q4Team<WIDE>::THREADS, 1) decode_q4_kernel(con
                 const uint32_t c0 = hmul2(b[j][i][0], sv.x), c1 = hmul2(b[j][i][1], sv.y);
                 q4_mma(o[j][2 * q], r0 & kNibLo, r0 & kByte, r08 & kNibLo, r08, c0, c1);
                 q4_mma(o[j][2 * q + 1], r1 & kNibLo, r1 & kByte, r18 & kNibLo, r18, c0, c1);
-                q4_mma(ov[j][q], of[0], of[1], of[2], of[3], c0, c1);
               }
             }
           }
