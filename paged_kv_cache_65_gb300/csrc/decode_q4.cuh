@@ -201,6 +201,23 @@ __device__ __forceinline__ bool q4_wait(uint64_t* bar, uint32_t parity) {
   return true;
 }
 
+// q4_wait for the producer, whose ring gives it time: it sleeps between tries
+__device__ __forceinline__ bool q4_wait_idle(uint64_t* bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer_ns();
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) return false;
+    __nanosleep(300);
+  }
+}
 template <int D, bool WIDE>
 constexpr int decode_q4_team_bytes() {
   using C = Q4Cfg<D>;
@@ -413,7 +430,7 @@ __global__ void __launch_bounds__(Q4Team<WIDE>::THREADS, 1) decode_q4_kernel(con
         const int slot = stage % NST;
         unsigned char* dst = st + slot * C::STAGE_BYTES + (lane & 15) * unit_bytes;
         if (stage >= NST && alive) {
-          if (!q4_wait(&empty[slot], ((stage / NST) & 1) ^ 1)) {
+          if (!q4_wait_idle(&empty[slot], ((stage / NST) & 1) ^ 1)) {
             alive = false;
             if (lane == 0) record_status(a.status, 8);
           }
@@ -598,7 +615,7 @@ __global__ void __launch_bounds__(Q4Team<WIDE>::THREADS, 1) decode_q4_kernel(con
       qoff[j] = pack_f16(u0, u1);
       if (t >= 2) qoff[j] = pack_f16(u0 - half_lo(qoff[j]), u1 - half_hi(qoff[j]));
     }
-    Offsets at = offsets(wt * 32);
+    Offsets at = offsets((wt & 1) * 32);
     // WIDE: the fragments go through shared memory, which leaves the registers to
     // O; the warps of a set hold the same ones
     const uint32_t q_addr = smem_u32(q_frag) + ((warp % NP) * NTW * GR * 32 + lane) * 16;
@@ -655,20 +672,23 @@ __global__ void __launch_bounds__(Q4Team<WIDE>::THREADS, 1) decode_q4_kernel(con
       }
       alive = __all_sync(0xffffffffu, alive);  // reconverge before ldmatrix / mma.sync
       const int nvalid = p.tok_end - tok0 < C::TS ? p.tok_end - tok0 : C::TS;
-      const uint32_t kb = k_base + slot * C::STAGE_BYTES;
-      const uint32_t vb = kb + NST * C::STAGE_BYTES;
       // two 16-token tiles a pass: their chains of MMAs interleave, and one
       // check of the running maximum covers both
 #pragma unroll 1
       for (int tb = wt * 32; tb < nvalid; tb += WT * 32) {
         const int nv = nvalid - tb;  // tokens of the pass inside the context (>= 1)
-        if (tb != at.tb) at = offsets(tb);
+        // 64 tokens on are whole units on: only a warp that takes every pass (WT =
+        // 1) meets other offsets
+        if ((tb & 32) != at.tb) at = offsets(tb & 32);
+        const uint32_t kb =
+            k_base + slot * C::STAGE_BYTES + (tb >> 6) * ((64 >> lur) * unit_bytes);
+        const uint32_t vb = kb + NST * C::STAGE_BYTES;
         // past the context: V scales zero, whatever the bytes hold (a NaN times
         // a zero weight would reach the sum).  This warp alone reads them, the
         // fence orders the writes before the copy that refills the stage.
         if (nv < 32) {
           if (lane >= nv) {
-            const int r = tb + lane;
+            const int r = (tb & 32) + lane;
             const uint32_t sa = vb + unit_of(r) + GR * UR * 16 + row_of(r) * 2;
 #pragma unroll
             for (int q = 0; q < GR; ++q)
