@@ -264,6 +264,16 @@ __global__ void __launch_bounds__(Q4Team<WIDE>::THREADS, 1) decode_q4_kernel(con
   constexpr int lur = ilog2(UR);
   constexpr uint32_t unit_bytes = static_cast<uint32_t>(UR) * C::ROW;
 
+  const bool use_rec = PLAN && a.starts != nullptr && a.start_grid == a.grid;
+  if (is_producer) {
+    // tables and lengths that kernels before this one write (a pool with device
+    // tables) are read only after them; host-written ones before the wait, as in
+    // decode_mma.cuh
+    if (a.meta_wait) griddep_wait();
+    if (use_rec && team < T::TEAMS)
+      reinterpret_cast<int32_t*>(rec_s)[lane] =
+          reinterpret_cast<const int32_t*>(a.starts + cta)[lane];
+  }
   if (is_producer && team < T::TEAMS && lane == 0) {
     for (int i = 0; i < NST; ++i) {
       mbar_init(&full[i], 1);
@@ -290,11 +300,6 @@ __global__ void __launch_bounds__(Q4Team<WIDE>::THREADS, 1) decode_q4_kernel(con
     // ------------------------------------------------------------ producer
     reg_dealloc<T::REGS_P>();
     if (team >= T::TEAMS) return;  // a warp without a team
-    // tables and lengths that kernels before this one write (a pool with device
-    // tables) are read only after them; host-written ones before the wait, as in
-    // decode_mma.cuh
-    if (a.meta_wait) griddep_wait();
-    const bool use_rec = PLAN && a.starts != nullptr && a.start_grid == a.grid;
     PieceWalker pw;
     PlanWalker plw;
     if constexpr (PLAN) {
@@ -308,13 +313,7 @@ __global__ void __launch_bounds__(Q4Team<WIDE>::THREADS, 1) decode_q4_kernel(con
       plw.r = r0;
       plw.r1 = r0 + chunk < W ? r0 + chunk : W;
       plw.s = 0;
-      if (use_rec) {
-        reinterpret_cast<int32_t*>(rec_s)[lane] =
-            reinterpret_cast<const int32_t*>(a.starts + cta)[lane];
-        __syncwarp();
-      } else {
-        plw.s = r0 < W ? plan_find(a.segs, a.n_segs, r0) : a.n_segs;
-      }
+      if (!use_rec) plw.s = r0 < W ? plan_find(a.segs, a.n_segs, r0) : a.n_segs;
     } else {
       const WalkStart w = find_start(a.ctx, a.n_seq, B, H, a.max_blocks, a.grid, cta, a.status);
       const long long r0 = (long long)cta * w.chunk;
@@ -488,7 +487,8 @@ __global__ void __launch_bounds__(Q4Team<WIDE>::THREADS, 1) decode_q4_kernel(con
     if constexpr (PLAN) {
       const int mi = col / G;
       gi = col - mi * G;
-      seqm = colv ? a.members[pc.mem + mi] : 0;
+      // the first member is the piece's own row
+      if (mi > 0) seqm = colv ? a.members[pc.mem + mi] : 0;
     }
     const uint4* qw = reinterpret_cast<const uint4*>(
         static_cast<const unsigned char*>(a.q) +
