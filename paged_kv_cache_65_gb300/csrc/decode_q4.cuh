@@ -61,7 +61,7 @@ struct Q4Team {
   static constexpr int NST = WIDE ? 5 : 3;                // stages in a team's ring
   static constexpr int THREADS = (TEAMS + 1) * 128;
   // registers a thread: at launch, consumers, producers
-  static constexpr int REGS = WIDE ? 168 : 128, REGS_C = WIDE ? 224 : 152, REGS_P = 56;
+  static constexpr int REGS = WIDE ? 168 : 128, REGS_C = WIDE ? 216 : 144, REGS_P = WIDE ? 72 : 80;
   static_assert(TEAMS * REGS_C + REGS_P <= (TEAMS + 1) * REGS, "setmaxnreg waits for registers");
 };
 
@@ -369,8 +369,9 @@ __global__ void __launch_bounds__(Q4Team<WIDE>::THREADS, 1) decode_q4_kernel(con
     int stage = 0;
     TableCache tc;
     tc.ent = tcache;
-    // pieces go to the consumers as descriptors, published one piece ahead of
-    // their copies (see decode_mma.cuh); rep = -1 ends the list
+    // pieces go to the consumers as descriptors, published after the first
+    // copies of the piece before (finding one reads the plan or the lengths);
+    // rep = -1 ends the list
     int npub = 0;
     auto publish = [&](const Piece& x, bool valid) {
       const int di = npub % kPieceRing;
@@ -395,64 +396,71 @@ __global__ void __launch_bounds__(Q4Team<WIDE>::THREADS, 1) decode_q4_kernel(con
     unsigned char* st = lane < 16 ? k_st : v_st;
     const long long pool_row = (long long)a.layer * a.n_blocks * H;  // chunks before the layer
     Piece p, pn;
+    // lanes 0 .. 15 bring the K units of a slot, lanes 16 .. 31 the V units;
+    // where a unit is goes before the wait for the slot, and no division by the
+    // block size is on the way (KU = 1 for blocks of up to 64 tokens)
+    auto copy_slot = [&](int u0, int u_last) {
+      const int u = u0 + (lane & 15);
+      const int n_units = min(u_last + 1 - u0, UPS);
+      const bool mine = (lane & 15) < n_units;
+      const int j0 = KU == 1 ? u0 : u0 / KU, jl = KU == 1 ? u0 + n_units - 1 : (u0 + n_units - 1) / KU;
+      const int j = KU == 1 ? u : u / KU;
+      const int row = KU == 1 ? 0 : (u - j * KU) * UR;
+      // the first slot of the record's piece takes the record's block ids
+      const bool from_rec = use_rec && stage == 0 && p.seg == rec_s->seg && j0 >= rec_s->b0 &&
+                            jl - rec_s->b0 < rec_s->n_pid;
+      if (!from_rec) tc.ensure(a.table, a.max_blocks, p.rep, j0, jl, lane);
+      int pid = 0;
+      if (mine) pid = from_rec ? rec_s->pid[j - rec_s->b0] : tc.ent[j - tc.base];
+      if (pid < 0 || pid >= a.n_blocks) {
+        record_status(a.status, 1);
+        pid = 0;  // stay in bounds; the result is flagged as invalid
+      }
+      const unsigned char* src = pool + (pool_row + static_cast<long long>(pid) * H + p.head) *
+                                            static_cast<long long>(B * C::ROW);
+      const int slot = stage % NST;
+      unsigned char* dst = st + slot * C::STAGE_BYTES + (lane & 15) * unit_bytes;
+      if (stage >= NST && alive) {
+        if (!q4_wait_idle(&empty[slot], ((stage / NST) & 1) ^ 1)) {
+          alive = false;
+          if (lane == 0) record_status(a.status, 8);
+        }
+      }
+      if (lane == 0) mbar_arrive_expect_tx(&full[slot], 2u * n_units * unit_bytes);
+      __syncwarp();
+      if (mine) {
+        if (KU == 1) {
+          bulk_load(dst, src, unit_bytes, &full[slot]);
+        } else {  // part of a larger block: plane by plane
+#pragma unroll
+          for (int q = 0; q < GR; ++q) {
+            bulk_load(dst + q * UR * 16, src + (q * B + row) * 16, UR * 16, &full[slot]);
+            if (lane >= 16)
+              bulk_load(dst + GR * UR * 16 + q * UR * 2, src + GR * B * 16 + (q * B + row) * 2,
+                        UR * 2, &full[slot]);
+          }
+          if (lane < 16)
+            bulk_load(dst + GR * UR * 16, src + GR * B * 16 + row * GR * 2, UR * GR * 2,
+                      &full[slot]);
+        }
+      }
+      ++stage;
+    };
     bool have = next_piece(p);
     if (have && !use_rec) tc.ensure(a.table, a.max_blocks, p.rep, p.b0, p.b0, lane);
     wait_previous_grid();
     publish(p, have);
     while (have) {
-      const bool have_next = next_piece(pn);
-      publish(pn, have_next);
-      // lanes 0 .. 15 bring the K units of a slot, lanes 16 .. 31 the V units;
-      // where a unit is goes before the wait for the slot, and no division by
-      // the block size is on the way (KU = 1 for blocks of up to 64 tokens)
+      bool have_next = false;
       const int u_first = p.b0 * KU;
       const int u_last = u_first + ((p.tok_end - p.b0 * B + UR - 1) >> lur) - 1;
-      for (int u0 = u_first; u0 <= u_last; u0 += UPS) {
-        const int u = u0 + (lane & 15);
-        const int n_units = min(u_last + 1 - u0, UPS);
-        const bool mine = (lane & 15) < n_units;
-        const int j0 = KU == 1 ? u0 : u0 / KU, jl = KU == 1 ? u0 + n_units - 1 : (u0 + n_units - 1) / KU;
-        const int j = KU == 1 ? u : u / KU;
-        const int row = KU == 1 ? 0 : (u - j * KU) * UR;
-        // the first slot of the record's piece takes the record's block ids
-        const bool from_rec = use_rec && stage == 0 && p.seg == rec_s->seg && j0 >= rec_s->b0 &&
-                              jl - rec_s->b0 < rec_s->n_pid;
-        if (!from_rec) tc.ensure(a.table, a.max_blocks, p.rep, j0, jl, lane);
-        int pid = 0;
-        if (mine) pid = from_rec ? rec_s->pid[j - rec_s->b0] : tc.ent[j - tc.base];
-        if (pid < 0 || pid >= a.n_blocks) {
-          record_status(a.status, 1);
-          pid = 0;  // stay in bounds; the result is flagged as invalid
+      // (a piece may hold no block: work units are finer)
+      for (int u0 = u_first; u0 <= u_last || u0 == u_first; u0 += UPS) {
+        if (u0 <= u_last) copy_slot(u0, u_last);
+        if (u0 == u_first) {
+          have_next = next_piece(pn);
+          publish(pn, have_next);
         }
-        const unsigned char* src = pool + (pool_row + static_cast<long long>(pid) * H + p.head) *
-                                              static_cast<long long>(B * C::ROW);
-        const int slot = stage % NST;
-        unsigned char* dst = st + slot * C::STAGE_BYTES + (lane & 15) * unit_bytes;
-        if (stage >= NST && alive) {
-          if (!q4_wait_idle(&empty[slot], ((stage / NST) & 1) ^ 1)) {
-            alive = false;
-            if (lane == 0) record_status(a.status, 8);
-          }
-        }
-        if (lane == 0) mbar_arrive_expect_tx(&full[slot], 2u * n_units * unit_bytes);
-        __syncwarp();
-        if (mine) {
-          if (KU == 1) {
-            bulk_load(dst, src, unit_bytes, &full[slot]);
-          } else {  // part of a larger block: plane by plane
-#pragma unroll
-            for (int q = 0; q < GR; ++q) {
-              bulk_load(dst + q * UR * 16, src + (q * B + row) * 16, UR * 16, &full[slot]);
-              if (lane >= 16)
-                bulk_load(dst + GR * UR * 16 + q * UR * 2, src + GR * B * 16 + (q * B + row) * 2,
-                          UR * 2, &full[slot]);
-            }
-            if (lane < 16)
-              bulk_load(dst + GR * UR * 16, src + GR * B * 16 + row * GR * 2, UR * GR * 2,
-                        &full[slot]);
-          }
-        }
-        ++stage;
       }
       p = pn;
       have = have_next;

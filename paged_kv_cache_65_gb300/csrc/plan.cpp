@@ -58,17 +58,19 @@ Layout plan_layout(int n_seq, int H, int n_segs, int n_members, int n_entries, i
 
 // CTA count of the split pass for the plan's kernel: the count the launcher
 // has settled on for this pool, else the kernel's design occupancy (two CTAs
-// per SM for the warp-level MMA pass, one for the tcgen05 pass) once the
-// device is known, else 0 (no start records).  A record set built for another
+// per SM for the warp-level MMA pass, one for the tcgen05 pass; a q4_0 pool's
+// pass counts teams, three per SM in its narrow form and two in its wide one)
+// once the device is known, else 0 (no start records).  A record set built for another
 // count than the launch's is ignored by the kernels.
 int plan_grid(const kvPool* p, int kernel, int G) {
   if (p->plan_grid > 0) return p->plan_grid < kMaxDecodeCtas ? p->plan_grid : kMaxDecodeCtas;
+  const bool q4 = p->dtype == KV_DTYPE_Q4_0;
   int g = 0;
   if (kernel == kPlanKernelTc) {
-    g = p->grid_tc > 0 ? p->grid_tc : pool_sm_count(p);
+    g = p->grid_tc > 0 ? p->grid_tc : (q4 ? 2 : 1) * pool_sm_count(p);
   } else {
     const int lg = G <= 1 ? 0 : (G == 2 ? 1 : (G == 4 ? 2 : 3));
-    g = p->grid_by_g[lg] > 0 ? p->grid_by_g[lg] : 2 * pool_sm_count(p);
+    g = p->grid_by_g[lg] > 0 ? p->grid_by_g[lg] : (q4 ? 3 : 2) * pool_sm_count(p);
   }
   return g < kMaxDecodeCtas ? g : kMaxDecodeCtas;
 }
