@@ -18,7 +18,7 @@ namespace pkv {
 namespace {
 
 constexpr int kScanThreads = 1024;
-constexpr int kFillThreads = 256, kFillAhead = 4;
+constexpr int kFillThreads = 256, kFillAhead = 8;
 constexpr int kMaxRows = 1 << 20;  // rows of a table set: one bit each in shared memory
 
 // Workspace: the batch's verdict and the ring position it starts at, then one
@@ -109,6 +109,18 @@ __global__ void __launch_bounds__(kScanThreads, 1) tables_scan_kernel(const Tabl
   __shared__ int bad;
   griddep_wait();
   griddep_launch_dependents();
+  // everything the first 1024 rows need is on its way before the bits are clear
+  const int64_t head = a.free_state[0], count = a.free_state[1];
+  int r = -1, old = 0, cnt = 0;
+  auto load_row = [&](int i) {
+    r = -1;
+    old = cnt = 0;
+    if (i >= a.n_seq) return;
+    if (!RELEASE) cnt = a.counts ? a.counts[i] : 1;
+    r = batch_row(a, i);
+    if (r >= 0) old = a.lens[r];
+  };
+  load_row(threadIdx.x);
   const int words = (a.n_rows + 31) / 32;
   for (int i = threadIdx.x; i < words; i += kScanThreads) seen[i] = 0;
   if (threadIdx.x == 0) bad = 0;
@@ -118,12 +130,8 @@ __global__ void __launch_bounds__(kScanThreads, 1) tables_scan_kernel(const Tabl
   for (int base = 0; base < a.n_seq; base += kScanThreads) {
     const int i = base + threadIdx.x;
     int64_t nb = 0, nt = 0;
-    int old = 0;
     if (i < a.n_seq) {
-      const int r = batch_row(a, i);
       if (r >= 0) {
-        old = a.lens[r];
-        const int cnt = RELEASE ? 0 : (a.counts ? a.counts[i] : 1);
         const bool dup = (atomicOr(&seen[r >> 5], 1u << (r & 31)) >> (r & 31)) & 1u;
         if (dup || old < 0 || old > room || cnt < 0 || static_cast<int64_t>(old) + cnt > room) {
           bad = 1;
@@ -145,9 +153,9 @@ __global__ void __launch_bounds__(kScanThreads, 1) tables_scan_kernel(const Tabl
                           static_cast<int32_t>(blocks + nb), static_cast<int32_t>(tokens + nt)};
     blocks += tb;
     tokens += tt;
+    if (base + kScanThreads < a.n_seq) load_row(i + kScanThreads);
   }
   __syncthreads();
-  const int64_t head = a.free_state[0], count = a.free_state[1];
   int why = bad ? KV_DEV_BAD_TABLE_ROW : 0;
   if (head < 0 || head >= a.free_cap || count < 0 || count > a.free_cap)
     why |= KV_DEV_BAD_TABLE_ROW;
@@ -231,13 +239,15 @@ __global__ void __launch_bounds__(kFillThreads) tables_fill_kernel(const TablesA
     if (a.positions) a.positions[t] = pos;
     return;
   }
-  const int w = blockIdx.x - n_tok_ctas;
-  const int i = w / parts, part = w - i * parts;
+  const unsigned w = blockIdx.x - n_tok_ctas;
+  const int i = w / static_cast<unsigned>(parts), part = w - i * parts;
   const RowPlan p = a.plan[i];
   const int r = batch_row(a, i);
   const bool live = h.ok && r >= 0;
-  const int ob = live ? (p.old_len + a.B - 1) / a.B : 0;
-  const int nb = live ? static_cast<int>((static_cast<int64_t>(p.old_len) + p.n + a.B - 1) / a.B) : 0;
+  // below 2^32: a row's room is below 2^31 tokens
+  const unsigned uB = a.B, end = static_cast<unsigned>(p.old_len) + p.n;
+  const int ob = live ? static_cast<int>((p.old_len + uB - 1) / uB) : 0;
+  const int nb = live ? static_cast<int>((end + uB - 1) / uB) : 0;
   int32_t* row = live ? a.tables + static_cast<int64_t>(r) * a.max_blocks : nullptr;
   int32_t* out = a.block_table ? a.block_table + static_cast<int64_t>(i) * a.max_blocks : nullptr;
   const int j0 = out ? 0 : ob, j1 = out ? a.max_blocks : nb;
@@ -329,10 +339,11 @@ cudaError_t launch_scan(bool pdl, const TablesArgs& a, cudaStream_t st) {
   return launch_kernel(pdl, tables_scan_kernel<RELEASE>, dim3(1), dim3(kScanThreads), smem, st, a);
 }
 
-// CTAs per row: one for each kFillAhead * kFillThreads entries, at most eight.
+// CTAs per row: one for each kFillAhead * kFillThreads entries (to the nearest:
+// a CTA goes round for what is left), at most eight.
 int row_parts(int max_blocks) {
   const int per = kFillAhead * kFillThreads;
-  const int want = (max_blocks + per - 1) / per;
+  const int want = max_blocks / per + (max_blocks % per > per / 2);
   return want < 1 ? 1 : (want > 8 ? 8 : want);
 }
 
