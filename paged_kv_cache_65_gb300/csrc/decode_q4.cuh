@@ -89,6 +89,7 @@ __device__ __forceinline__ int q4_srow(int k) { return 4 * ((k >> 1) & 3) + 2 * 
 __device__ __forceinline__ int q4_vrow(int i) { return (i & ~3) + 2 * (i & 1) + ((i >> 1) & 1); }
 
 constexpr uint32_t kNibLo = 0x000f000fu;  // n * 2^-24
+constexpr uint32_t kNibHi = 0x00f000f0u;  // n * 2^-20
 constexpr uint32_t kByte = 0x00ff00ffu;   // (16 n' + n) * 2^-24, n' the high nibble
 
 // Headroom of a column's largest weight over the maximum that set it, in
@@ -563,10 +564,8 @@ __global__ void __launch_bounds__(Q4Team<WIDE>::THREADS, 1) decode_q4_kernel(con
     const int wt = warp / NP;
     // Q fragments.  Column g is scaled by the power of two that brings its
     // largest |q| into [2^14, 2^15): bf16's 8 bits then stay exact in fp16
-    // over 2^28 of range.  MMA 1 of a group takes whole bytes 16 n' + n (n' the
-    // odd dimension's nibble) with Q' / 16 as the factors, MMA 0 the low nibbles
-    // n with Q - Q' / 16, which takes the rest off again (rounded to fp16's 11
-    // bits, three more than q has).
+    // over 2^28 of range.  MMA 0 of a group takes dimensions 8t + {0, 4} and
+    // {2, 6}, MMA 1 (the nibbles times 16) 8t + {1, 5} and {3, 7} over 16.
     uint32_t qf[NTW][GR][4];
     uint32_t qoff[NTW];   // offset fragment, see below
     float fcol[NTW][2];   // score factors of columns 2t and 2t + 1
@@ -600,16 +599,15 @@ __global__ void __launch_bounds__(Q4Team<WIDE>::THREADS, 1) decode_q4_kernel(con
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u) * sc * 0.0625f;
-          x[2 * i] = __uint_as_float(w[i] << 16) * sc - x[2 * i + 1];
+          x[2 * i] = __uint_as_float(w[i] << 16) * sc;
         }
         qx[0] = pack_f16(x[0], x[4]);
         qx[1] = pack_f16(x[2], x[6]);
         qx[2] = pack_f16(x[1], x[5]);
         qx[3] = pack_f16(x[3], x[7]);
-        // the offset's sum, 8 Q0 + 136 Q1, takes the values the MMAs take (as
-        // rounded)
+        // the offset's sum takes the values the MMAs take (as rounded)
         float sum = (half_lo(qx[0]) + half_hi(qx[0])) + (half_lo(qx[1]) + half_hi(qx[1]));
-        sum += 17.f * ((half_lo(qx[2]) + half_hi(qx[2])) + (half_lo(qx[3]) + half_hi(qx[3])));
+        sum += 16.f * ((half_lo(qx[2]) + half_hi(qx[2])) + (half_lo(qx[3]) + half_hi(qx[3])));
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
         off[q] = sum * (-8.f * 0x1p-24f);  // below 1: |q| < 2^15
@@ -739,7 +737,7 @@ __global__ void __launch_bounds__(Q4Team<WIDE>::THREADS, 1) decode_q4_kernel(con
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const uint32_t wa = w[2 * i], wb = w[2 * i + 1];
-              const uint32_t wa8 = q4_odd_bytes(wa), wb8 = q4_odd_bytes(wb);
+              const uint32_t wa8 = wa >> 8, wb8 = wb >> 8;
               const float fl = q & 1 ? half_hi(sc[i][0][q / 2]) : half_lo(sc[i][0][q / 2]);
               const float fh = q & 1 ? half_hi(sc[i][1][q / 2]) : half_lo(sc[i][1][q / 2]);
 #pragma unroll
@@ -747,7 +745,7 @@ __global__ void __launch_bounds__(Q4Team<WIDE>::THREADS, 1) decode_q4_kernel(con
                 float acc[4];
                 q4_mma_z(acc, wa & kNibLo, wb & kNibLo, wa8 & kNibLo, wb8 & kNibLo, fq[j].x,
                          fq[j].y);
-                q4_mma(acc, wa & kByte, wb & kByte, wa8, wb8, fq[j].z, fq[j].w);
+                q4_mma(acc, wa & kNibHi, wb & kNibHi, wa8 & kNibHi, wb8 & kNibHi, fq[j].z, fq[j].w);
                 s[j][i][0] = fmaf(fl, acc[0], s[j][i][0]);
                 s[j][i][1] = fmaf(fl, acc[1], s[j][i][1]);
                 s[j][i][2] = fmaf(fh, acc[2], s[j][i][2]);

@@ -80,12 +80,12 @@ def test_device_tables_option(lib):
             c.kv_pool_set_option(lib.KV_OPT_DEVICE_TABLES, v)
 
 
-@pytest.mark.parametrize("D,path,kernel", [(64, 0, 2), (64, 2, 2), (64, 3, 2), (128, 2, 2), (128, 3, 3)])
+@pytest.mark.parametrize("D,path,kernel", [(64, 0, 3), (64, 2, 2), (64, 3, 3), (128, 0, 3), (128, 2, 2), (128, 3, 3)])
 def test_plans_follow_the_decode_path(lib, D, path, kernel):
     from paged_kv_cache_65_gb300 import PagedKVCache
     from paged_kv_cache_65_gb300.cache import parse_plan
 
-    # the tcgen05 pass takes D_h = 128
+    # two sharers of two heads each: segments of 6 columns beside one of 12? no:
     c = PagedKVCache(1, 64, 16, 2, D, "q4_0", allocate=False)
     c.kv_pool_set_option(lib.KV_OPT_DECODE_PATH, path)
     c.seq_append_tokens(0, 512)
