@@ -152,16 +152,18 @@ kvStatus kv_block_refcount(const kvPool* pool, int32_t id, int* out);
 /* Pool options.  KV_OPT_DECODE_PATH selects the split-pass kernel:
  * 0 = automatic (warp-level tensor-core pass for bfloat16 pools whose block
  * size is a multiple of 8 and for FP8, q8_0 and q4_0 pools, CUDA-core pass
- * otherwise), 1 = always the CUDA-core pass (not for FP8, q8_0 or q4_0 pools), 2 =
- * the warp-level tensor-core pass (mma.sync) where the pool allows it, 3 =
- * the tcgen05 pass (tensor-memory accumulators; bfloat16 or FP8, D_h = 128)
- * where the pool allows it, else as 2.  A plan (paged_decode_plan)
- * records the kernel it was built for and the planned calls run that kernel;
- * in automatic mode the plan takes the tcgen05 pass when segments wider than
- * 16 query columns hold at least half of the blocks it reads, else the
- * warp-level pass.  Changing the option invalidates partials of earlier split
- * passes.  KV_OPT_PDL: 1 (default) =
- * launch kernels with a programmatic dependency on the previous grid in the
+ * otherwise), 1 = always the CUDA-core pass (not for FP8, q8_0 or q4_0
+ * pools), 2 = the warp-level tensor-core pass (mma.sync) where the pool
+ * allows it, 3 = the tcgen05 pass (tensor-memory accumulators; bfloat16 or
+ * FP8, D_h = 128) where the pool allows it, else as 2; plans of q4_0 pools:
+ * 2 = the warp-level pass's narrow form, 3 = its wide form (16 query columns
+ * a warp).  A plan (paged_decode_plan) records the kernel it was built for
+ * and the planned calls run that kernel; in automatic mode the plan takes the
+ * tcgen05 pass when segments wider than 16 query columns hold at least half
+ * of the blocks it reads, else the warp-level pass (q4_0 pools the wide form,
+ * with D_h = 128 from 9 columns on).  Changing the option invalidates
+ * partials of earlier split passes.  KV_OPT_PDL: 1 (default) = launch kernels
+ * with a programmatic dependency on the previous grid in the
  * stream (each kernel waits for its predecessors before reading their
  * results, but is scheduled while they finish), 0 = plain launches.
  * KV_OPT_PLAN_GRID: the CTA count for which paged_decode_plan writes its

@@ -10,23 +10,23 @@
 // groups q = 0 .. D/32 - 1:
 //     S[t]  = sum_q ks[t][q] * (sum_{d in q} n[t][d] Q[d] - 8 sum_{d in q} Q[d])
 //     O[d]  = sum_t n[t][d] P'[t][q] - 8 sum_t P'[t][q],  P'[t][q] = p[t] vs[t][q]
-// so both products run on the nibbles themselves.  The offset 8 costs S one MMA
-// per tile (the scales times the groups' sums of Q); for O every MMA of
-// nibbles is followed by one whose A operand is -8 throughout, into the same
-// accumulator, which so never holds more than a tile's offset beside the
-// signed sum (summed apart over a long piece the two would cancel to a small
-// rest of large sums: 1.8x the error at 32,771 tokens).
+// so both products run on the nibbles themselves, and the offset 8 is a small
+// product of the scales apart from them: for S the scales times the groups'
+// sums of Q, one MMA per tile and n-tile; for O the scales' transpose times p,
+// likewise, for all groups at once.
 //
 // Nibbles become fp16 MMA operands with one AND each: the fp16 bit pattern n
 // (n < 16, exponent bits zero) is the subnormal n * 2^-24, and n << 4 is
-// n * 2^-20, both exact MMA inputs.  A 32-bit word of eight nibbles gives four
-// operand registers in five instructions (four ANDs, one shift); the factors
-// 2^-24 and 16 go into Q (scaled per column by a power of two, so that any
-// magnitude of q stays inside fp16) and into the final scale of O.
+// n * 2^-20, both exact MMA inputs.  The factors 2^-24 and 16 go into Q (scaled
+// per column by a power of two, so that any magnitude of q stays inside fp16)
+// and into the final scale of O.
 //
 // MMAs are m16n8k16 (fp16 in, f32 accumulate) per 16-token tile:
 //     S^T [16 tokens x 8 cols] = K [16 x 32] . Q^T [32 x 8]   two per group
 //     O^T [32 x 8 cols]       += V^T [32 x 16] . P'^T [16 x 8] two per group
+// (e4m3 operands would take the nibbles with half the masks, but mma.sync of
+// e4m3 converts them to fp16 here and ran slower: 49 against 43 us for the
+// 131,071 tokens below.)
 // A group's 32 dimensions of one token are 16 consecutive bytes, so the
 // 16-bit ldmatrix hands lane (g, t) word t of token row g: nibbles of
 // dimensions 8t .. 8t + 7.  The sum over dimensions does not depend on their
@@ -41,6 +41,22 @@
 // are adjacent 16-byte vectors, so every 8-row phase of both ldmatrix forms
 // reads 8 different bank groups without a swizzle, and a block that is a
 // whole unit arrives in one bulk copy.
+//
+// What bounds it.  Narrow form (segments of up to 8 columns, three teams an
+// SM): memory.  A longer context adds time at 6.8 TB/s of codes and scales (a
+// pass that only copies: 7.0), and what is left of a call is its start, the
+// pieces' ends and the merge pass, 8.7 us at 333 tokens.  37 sequences of 2K
+// tokens, 8 K/V heads of 4 query heads: 27 us, 24 without any arithmetic;
+// 131,071 tokens, 8 heads of 8: 40 us, 36 without arithmetic.  It took 30 and 43
+// us with CTAs of 5 warps instead of teams: 128 registers a thread spilled, and
+// the compiler could not overlap the tile's chains.
+// Wide form (up to 32 columns, two teams an SM): instruction issue.  A pass of
+// 32 tokens by 16 columns is 72 MMAs and about 420 other instructions, 1,250
+// cycles with two warps a scheduler, the tensor pipe busy 46% of them.  12
+// prefixes of 32,771 tokens by 32 columns: 210 us; with one n-tile a warp (the
+// narrow form, unpacking everything four times) 298 us, with K and V converted
+// to fp16 for tcgen05 (tensor and shared memory traffic for every value, roles
+// waiting for one another) 276 us.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -53,7 +69,10 @@ constexpr int kQ4Warps = 4;  // consumer warps of a team
 
 // A CTA is several teams, each a CTA of the split by itself: four consumer
 // warps (a warpgroup), a producer warp, its own stages and work.  The producers
-// share the last warpgroup.  NTW: 8-column tiles a consumer warp holds at once.
+// share the last warpgroup and pass their registers to the consumers.  NTW:
+// 8-column tiles a consumer warp holds at once: two in the wide form, so that a
+// tile of K and V is read and unpacked half as often; its O then takes 64
+// registers, which leaves room for two teams (three spill: 304 against 229 us).
 template <bool WIDE>
 struct Q4Team {
   static constexpr int TEAMS = WIDE ? 2 : 3;

@@ -399,7 +399,11 @@ kvStatus plan_build(const kvPool* p, const int32_t* seq_ids, int n_seq, int n_q_
   // automatic: tcgen05 when segments of more than 16 columns hold at least
   // half of the blocks read (many sharers of long prefixes: its S and P.V
   // cost little per byte at any width), else the warp-level MMA pass (which
-  // streams narrow segments faster)
+  // streams narrow segments faster).  A q4_0 pool has the wide form of its pass
+  // in the place of tcgen05, from where it is faster: 12 prefixes of 16,387
+  // tokens, 8 K/V heads, narrow and wide form: D_h = 128 by 8 columns 54 and 68
+  // us, 12: 79 and 70, 16: 80 and 71, 32: 139 and 116; D_h = 64 by 16 columns 54
+  // and 58, 32: 90 and 81
   int kernel = kPlanKernelMma;
   if (pool_tc_decode_shape(p)) {
     if (p->decode_path == 3) {
@@ -408,7 +412,7 @@ kvStatus plan_build(const kvPool* p, const int32_t* seq_ids, int n_seq, int n_q_
       int64_t wide = 0, all = 0;
       for (const PlanSeg& s : segs) {
         all += s.b1 - s.b0;
-        if (s.ncols > (p->dtype == KV_DTYPE_Q4_0 ? 8 : 16)) wide += s.b1 - s.b0;
+        if (s.ncols > (p->dtype == KV_DTYPE_Q4_0 && p->D == 128 ? 8 : 16)) wide += s.b1 - s.b0;
       }
       if (all > 0 && 2 * wide >= all) kernel = kPlanKernelTc;
     }

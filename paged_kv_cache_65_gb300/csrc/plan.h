@@ -89,7 +89,7 @@ constexpr int plan_max_segs(int n_seq, int n_kv_heads) {
 // Split-pass kernels a plan can be built for (the values of the pool's
 // decode-path option).
 constexpr int kPlanKernelMma = 2;  // warp-level MMA (mma.sync)
-constexpr int kPlanKernelTc = 3;   // tcgen05, TMEM accumulators
+constexpr int kPlanKernelTc = 3;   // tcgen05, TMEM accumulators; q4_0: the wide form
 
 // Work units per block.  The split pass balances units.  On the warp-level
 // MMA kernel a block costs more the more 8-column n-tiles it carries (1, 2,

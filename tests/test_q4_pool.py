@@ -85,7 +85,7 @@ def test_plans_follow_the_decode_path(lib, D, path, kernel):
     from paged_kv_cache_65_gb300 import PagedKVCache
     from paged_kv_cache_65_gb300.cache import parse_plan
 
-    # two sharers of two heads each: segments of 6 columns beside one of 12? no:
+    # three sharers of eight query heads a K/V head: 24 columns; 3 = the wide form
     c = PagedKVCache(1, 64, 16, 2, D, "q4_0", allocate=False)
     c.kv_pool_set_option(lib.KV_OPT_DECODE_PATH, path)
     c.seq_append_tokens(0, 512)
