@@ -180,14 +180,15 @@ def ptr_f32(a: np.ndarray):
     return a.ctypes.data_as(_f32p)
 
 
-def vp(x) -> _vp:
-    """A device/host address from an int, a torch tensor or a NumPy array."""
-    if x is None:
-        return _vp(0)
-    if isinstance(x, int):
-        return _vp(x)
+def vp(x):
+    """A device/host address from an int, a torch tensor or a NumPy array, as
+    an argument of a ``void*`` parameter (None: null)."""
+    if x is None or type(x) is int:
+        return x
     if hasattr(x, "data_ptr"):
-        return _vp(x.data_ptr())
+        return x.data_ptr()
     if isinstance(x, np.ndarray):
-        return _vp(x.ctypes.data)
+        return x.ctypes.data
+    if isinstance(x, int):
+        return int(x)
     raise TypeError(type(x))

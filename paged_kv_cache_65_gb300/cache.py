@@ -20,19 +20,27 @@ DTYPES = {"f32": _lib.KV_DTYPE_F32, "bf16": _lib.KV_DTYPE_BF16, "fp8_e4m3": _lib
           "q8_0": _lib.KV_DTYPE_Q8_0, "q4_0": _lib.KV_DTYPE_Q4_0}
 
 
-def _stream(stream) -> C.c_void_p:
-    if stream is None:
-        try:
-            import torch
+_current_stream = None  # () -> raw handle of the current device's current stream
 
-            if torch.cuda.is_available():
-                return C.c_void_p(torch.cuda.current_stream().cuda_stream)
-        except Exception:  # pragma: no cover - torch always present here
-            pass
-        return C.c_void_p(0)
-    if isinstance(stream, int):
-        return C.c_void_p(stream)
-    return C.c_void_p(stream.cuda_stream)
+
+def _stream(stream) -> int:
+    """The stream's raw handle; None: torch's current stream, 0 without CUDA."""
+    global _current_stream
+    if stream is None:
+        if _current_stream is None:
+            try:
+                import torch
+
+                if not torch.cuda.is_available():
+                    return 0
+                raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+                dev = torch.cuda.current_device
+                _current_stream = (lambda: raw(dev())) if raw is not None else \
+                    (lambda: torch.cuda.current_stream().cuda_stream)
+            except Exception:  # pragma: no cover - torch always present here
+                return 0
+        return _current_stream()
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 class PagedKVCache:
@@ -484,19 +492,21 @@ def _addr(x) -> int:
 
 
 def _nbytes(t) -> int:
-    if hasattr(t, "numel"):
-        return t.numel() * t.element_size()
     return t.nbytes
 
 
-def _out_dtype(out) -> int:
-    import torch
+_OUT_DTYPES = {}
 
-    if out.dtype == torch.float32:
-        return _lib.KV_DTYPE_F32
-    if out.dtype == torch.bfloat16:
-        return _lib.KV_DTYPE_BF16
-    raise TypeError(out.dtype)
+
+def _out_dtype(out) -> int:
+    if not _OUT_DTYPES:
+        import torch
+
+        _OUT_DTYPES.update({torch.float32: _lib.KV_DTYPE_F32, torch.bfloat16: _lib.KV_DTYPE_BF16})
+    code = _OUT_DTYPES.get(out.dtype)
+    if code is None:
+        raise TypeError(out.dtype)
+    return code
 
 
 PLAN_SEG = np.dtype([("wpre", "<i8"), ("rep", "<i4"), ("b0", "<i4"), ("b1", "<i4"),
