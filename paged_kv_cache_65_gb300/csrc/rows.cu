@@ -196,6 +196,7 @@ __global__ void __launch_bounds__(256)
     if (threadIdx.x == 0) record_status(status, KV_DEV_BAD_SLOT);
     return;
   }
+  // a pool has fewer than 2^31 slots
   const uint32_t blk = static_cast<uint32_t>(slot) / static_cast<uint32_t>(ks.B);
   const int o = static_cast<int>(static_cast<uint32_t>(slot) - blk * ks.B);
   const int row = ks.H * ks.D / VEC;

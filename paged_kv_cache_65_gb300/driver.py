@@ -44,8 +44,19 @@ class TableRun:
         stage = cache.paged_prefill_staging_bytes(max_batch, max_blocks) if max_tokens else 0
         self._stage = torch.empty(stage, **u8) if stage else None
 
-    def _append(self, rows, counts, n_tokens, stream):
-        n = rows.numel()
+    def _append(self, rows, counts, n_tokens, q, k_new, v_new, out, stream):
+        n, c = rows.numel(), self.c
+        if n > self.lens.numel() or n_tokens > self.slots.numel():
+            raise ValueError("more rows or tokens than the run was made for")
+        kv = (c.L, n_tokens, c.H, c.D)
+        if (rows.dtype != torch.int32 or (counts is not None and (
+                counts.dtype != torch.int32 or counts.numel() != n))):
+            raise TypeError("rows and counts: int32, one count per row")
+        if tuple(k_new.shape) != kv or tuple(v_new.shape) != kv or \
+                tuple(q.shape) != (c.L, n_tokens, self.n_q_heads, c.D) or out.shape != q.shape or \
+                not all(x.is_contiguous() for x in (q, k_new, v_new, out, rows)):
+            raise ValueError("k_new, v_new [L, tokens, H_kv, D_h], q, out [L, tokens, H_q, D_h], "
+                             "contiguous")
         self.c.paged_tables_append(self.t, rows, counts, n, n_tokens, self.slots, self.positions,
                                    self.start, self.table, self.lens, workspace=self._ws,
                                    stream=stream)
@@ -56,7 +67,9 @@ class TableRun:
         rows and attend them over their contexts; ``out [L, n_tokens, H_q,
         D_h]``, rows past the last token left as they were."""
         c, n_tok = self.c, k_new.shape[1]
-        n = self._append(rows, counts, n_tok, stream)
+        if self._stage is None and c.paged_prefill_staging_bytes(1, self.mb):
+            raise ValueError("a run without max_tokens has no staging for prefill")
+        n = self._append(rows, counts, n_tok, q, k_new, v_new, out, stream)
         c.reshape_and_cache(-1, k_new, v_new, self.slots, n_tok, stream)
         for layer in range(c.L):
             c.paged_prefill_attention_staged(layer, q[layer], self.n_q_heads, self.table, self.mb,
@@ -68,7 +81,7 @@ class TableRun:
         """One decode step: a token for every listed row, padding entries last;
         ``out [L, n, H_q, D_h]``, zeros for padding entries."""
         c = self.c
-        n = self._append(rows, None, rows.numel(), stream)
+        n = self._append(rows, None, rows.numel(), q, k_new, v_new, out, stream)
         c.reshape_and_cache(-1, k_new, v_new, self.slots, n, stream)
         for layer in range(c.L):
             c.paged_decode_attention(layer, q[layer], self.n_q_heads, self.table, self.mb,

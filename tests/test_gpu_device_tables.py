@@ -365,3 +365,28 @@ def test_prefill_decode_release_loop_with_captured_steps(dtype):
     run.close()
     c.kv_pool_check()
     assert c.kv_pool_stats()[1] == 0
+
+
+def test_a_run_refuses_what_its_buffers_do_not_hold():
+    from paged_kv_cache_65_gb300 import PagedKVCache
+    from paged_kv_cache_65_gb300.driver import TableRun
+
+    c = PagedKVCache(1, 16, 16, 2, 128, "q4_0")
+    run = TableRun(c, 8, 4, 4, 8, 2)
+    rows = torch.tensor([0, 1], **I32)
+    kv = torch.zeros((1, 2, 2, 128), dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros((1, 2, 8, 128), dtype=torch.bfloat16, device="cuda")
+    out = torch.zeros((1, 2, 8, 128), device="cuda")
+    one = torch.tensor([1, 1], **I32)
+    with pytest.raises(ValueError):  # three rows in a run of two
+        run.step(torch.tensor([0, 1, 2], **I32), q, kv, kv, out)
+    with pytest.raises(ValueError):  # fewer values than rows
+        run.step(rows, q, kv[:, :1].contiguous(), kv, out)
+    with pytest.raises(ValueError):  # a run without staging
+        run.prefill(rows, one, 1, q, kv, kv, out)
+    with pytest.raises(TypeError):
+        run.step(rows.long(), q, kv, kv, out)
+    run.step(rows, q, kv, kv, out)
+    assert run.t.lens.cpu().tolist() == [1, 1, 0, 0]
+    assert c.kv_pool_device_status() == 0
+    run.close()

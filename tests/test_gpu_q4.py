@@ -266,7 +266,8 @@ def test_decode_of_ragged_contexts(G, B, D, path):
 
 
 @pytest.mark.parametrize("D,G,B,path", [(128, 4, 16, MMA), (64, 8, 16, MMA), (128, 8, 32, MMA), (128, 1, 8, MMA),
-                                        (128, 4, 16, WIDE), (128, 8, 32, WIDE), (128, 1, 8, WIDE), (128, 2, 192, WIDE)])
+                                        (128, 4, 16, WIDE), (128, 8, 32, WIDE), (128, 1, 8, WIDE), (128, 2, 192, WIDE),
+                                        (64, 8, 16, WIDE), (64, 4, 8, WIDE), (64, 2, 32, WIDE), (64, 8, 256, WIDE)])
 def test_fork_copy_on_write_and_the_planned_pass(D, G, B, path):
     # two steps over two layers: the first copies the shared, partly filled
     # tail of the forks; the shared prefix is read once through the plan
@@ -300,10 +301,10 @@ def test_fork_copy_on_write_and_the_planned_pass(D, G, B, path):
 
 
 @pytest.mark.parametrize("path", [MMA, WIDE])
-@pytest.mark.parametrize("n_br,G", [(3, 4), (4, 8), (8, 4), (5, 1)])
-def test_wide_shared_segments(n_br, G, path):
+@pytest.mark.parametrize("n_br,G,D", [(3, 4, 128), (4, 8, 128), (8, 4, 128), (5, 1, 128), (2, 8, 64), (4, 8, 64)])
+def test_wide_shared_segments(n_br, G, D, path):
     # segments of 12 to 32 columns: two and four n-tiles
-    B, H, D, prefix = 16, 2, 128, 1040
+    B, H, prefix = 16, 2, 1040
     n_blocks = prefix // B + 3 * n_br + 8
     ops = [("append", 100, prefix, 99)] + [("fork", 100, s) for s in range(n_br)]
     ops += [("append", s, 3 * s, s) for s in range(1, n_br)]
