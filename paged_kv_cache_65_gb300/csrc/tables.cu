@@ -6,6 +6,14 @@
 // the listed rows' new blocks and tokens, and commits lengths and the free
 // ring's state, or refuses the batch and changes nothing.  The second fills
 // what each listed row and token gets, spread over the device.
+//
+// What bounds them is latency: the scan's loads (row, then its length), two
+// scans over the CTA and the second kernel's start make 5.6 us for 37 rows of
+// 256 entries, whatever the bytes.  1,000 rows of 2,050 entries, 12 MB in and
+// out, take 9.2 us: the fill moves them with eight loads in flight a thread and
+// 32-bit divisions (four loads and 64-bit ones: 11.3 us).  Reading the rows
+// ahead of the wait for the scan gained nothing, nor did 16-byte vectors, which
+// rows of 2,050 entries do not allow.
 #include <cuda_runtime.h>
 
 #include <cstdint>
