@@ -13,7 +13,7 @@
 // so both products run on the nibbles themselves, and the offset 8 is a small
 // product of the scales apart from them: for S the scales times the groups'
 // sums of Q, one MMA per tile and n-tile; for O the scales' transpose times p,
-// likewise, for all groups at once.
+// likewise, for all groups at once, beside the sum of p itself.
 //
 // Nibbles become fp16 MMA operands with one AND each: the fp16 bit pattern n
 // (n < 16, exponent bits zero) is the subnormal n * 2^-24, and n << 4 is
@@ -45,15 +45,15 @@
 // What bounds it.  Narrow form (segments of up to 8 columns, three teams an
 // SM): memory.  A longer context adds time at 6.8 TB/s of codes and scales (a
 // pass that only copies: 7.0), and what is left of a call is its start, the
-// pieces' ends and the merge pass, 8.7 us at 333 tokens.  37 sequences of 2K
-// tokens, 8 K/V heads of 4 query heads: 27 us, 24 without any arithmetic;
-// 131,071 tokens, 8 heads of 8: 40 us, 36 without arithmetic.  It took 30 and 43
+// pieces' ends and the merge pass, 8.6 us at 333 tokens.  37 sequences of 2K
+// tokens, 8 K/V heads of 4 query heads: 26.7 us, 24 without any arithmetic;
+// 131,071 tokens, 8 heads of 8: 39.5 us, 36 without arithmetic.  It took 30 and 43
 // us with CTAs of 5 warps instead of teams: 128 registers a thread spilled, and
 // the compiler could not overlap the tile's chains.
 // Wide form (up to 32 columns, two teams an SM): instruction issue.  A pass of
 // 32 tokens by 16 columns is 72 MMAs and about 420 other instructions, 1,250
 // cycles with two warps a scheduler, the tensor pipe busy 46% of them.  12
-// prefixes of 32,771 tokens by 32 columns: 210 us; with one n-tile a warp (the
+// prefixes of 32,771 tokens by 32 columns: 214 us; with one n-tile a warp (the
 // narrow form, unpacking everything four times) 298 us, with K and V converted
 // to fp16 for tcgen05 (tensor and shared memory traffic for every value, roles
 // waiting for one another) 276 us.
@@ -72,7 +72,7 @@ constexpr int kQ4Warps = 4;  // consumer warps of a team
 // share the last warpgroup and pass their registers to the consumers.  NTW:
 // 8-column tiles a consumer warp holds at once: two in the wide form, so that a
 // tile of K and V is read and unpacked half as often; its O then takes 64
-// registers, which leaves room for two teams (three spill: 304 against 229 us).
+// registers, which leaves room for two teams (three spill and take as long).
 template <bool WIDE>
 struct Q4Team {
   static constexpr int TEAMS = WIDE ? 2 : 3;
@@ -532,9 +532,8 @@ __global__ void __launch_bounds__(Q4Team<WIDE>::THREADS, 1) decode_q4_kernel(con
   struct Offsets {
     int tb;
     uint32_t kc, vc;        // K and V codes (lane's row of the matrix loads)
-    uint32_t ks[2], vs;     // scales of K rows g, g + 8 and of V's four tokens
+    uint32_t ks, vs;        // scales of K row g (g + 8: two tokens on), of V's four tokens
     uint32_t vo;            // V scales of group g & 3 (rows of the offset's MMA)
-    uint32_t chk;           // V scales this lane checks: four tokens of a group
   };
   auto offsets = [&](int tb) -> Offsets {
     Offsets x;
@@ -543,16 +542,11 @@ __global__ void __launch_bounds__(Q4Team<WIDE>::THREADS, 1) decode_q4_kernel(con
     const int rv = tb + (lane >> 4) * 16 + q4_vrow(lane & 15);
     x.kc = unit_of(rk) + row_of(rk) * 16;
     x.vc = unit_of(rv) + row_of(rv) * 16;
-#pragma unroll
-    for (int hi = 0; hi < 2; ++hi) {
-      const int r = tb + q4_srow(g + 8 * hi);
-      x.ks[hi] = unit_of(r) + GR * UR * 16 + row_of(r) * GR * 2;
-    }
+    const int rs = tb + q4_srow(g);
+    x.ks = unit_of(rs) + GR * UR * 16 + row_of(rs) * GR * 2;
     const int rp = tb + 4 * t;  // four tokens never cross a unit
     x.vs = unit_of(rp) + GR * UR * 16 + row_of(rp) * 2;
     x.vo = x.vs + (g & (GR - 1)) * UR * 2;
-    const int rc = tb + 4 * (lane & 7);
-    x.chk = unit_of(rc) + GR * UR * 16 + ((lane >> 3) & (GR - 1)) * UR * 2 + row_of(rc) * 2;
     return x;
   };
   // from a pass's first tile to its second
@@ -655,21 +649,22 @@ __global__ void __launch_bounds__(Q4Team<WIDE>::THREADS, 1) decode_q4_kernel(con
       }
       named_bar_sync(1 + team, kQ4Warps * 32);
     }
-    float m_run[NTW][2], l_run[NTW][2];
+    float m_run[NTW][2];
     float e_run = kQ4Exp;  // weights are at most 2^e_run
     float o[NTW][C::MT][4];
 #pragma unroll
     for (int j = 0; j < NTW; ++j) {
       m_run[j][0] = m_run[j][1] = -INFINITY;
-      l_run[j][0] = l_run[j][1] = 0.f;
 #pragma unroll
       for (int mt = 0; mt < C::MT; ++mt) o[j][mt][0] = o[j][mt][1] = o[j][mt][2] = o[j][mt][3] = 0.f;
     }
     // The offset's part of O, -8 sum_t vs[t][q] p[t], is the same for every
     // dimension of a group: an MMA with the V scales as its rows, one for all
-    // groups (row q; those past the groups repeat them).  It is kept apart from O
-    // and added every few stages: summed apart over a long piece the two would
-    // cancel to a small rest of large sums (1.8x the error at 32,771 tokens).
+    // groups (rows 0 .. 3, row q & (GR - 1)); its row 4 is ones and sums the
+    // weights.  The offset is kept apart from O and added every few stages: summed
+    // apart over a long piece the two would cancel to a small rest of large sums
+    // (1.8x the error at 32,771 tokens).
+    const uint32_t one = g == 4 ? 0x3c003c00u : 0u, gm = g < 4 ? 0xffffffffu : 0u;
     float ov[NTW][2];
 #pragma unroll
     for (int j = 0; j < NTW; ++j) ov[j][0] = ov[j][1] = 0.f;
@@ -686,7 +681,7 @@ __global__ void __launch_bounds__(Q4Team<WIDE>::THREADS, 1) decode_q4_kernel(con
             o[j][2 * q][2 + k] = fmaf(x, -136.f * 0x1p-24f, o[j][2 * q][2 + k]);
             o[j][2 * q + 1][2 + k] = fmaf(x, -136.f * 0x1p-24f, o[j][2 * q + 1][2 + k]);
           }
-          ov[j][k] = 0.f;
+          if (g < 4) ov[j][k] = 0.f;
         }
     };
 
@@ -724,7 +719,11 @@ __global__ void __launch_bounds__(Q4Team<WIDE>::THREADS, 1) decode_q4_kernel(con
           fence_async_smem();
           __syncwarp();
         }
-        const uint2 chk = lds64(vb + at.chk);
+        // V scales of group g & 3 and four tokens of each tile: over the lanes all
+        // of the pass
+        uint2 so[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) so[i] = lds64(vb + at.vo + i * tile_vs);
         // ---- S^T = K . Q^T per tile: one accumulator per group, weighted by
         // its rows' K scales
         float s[NTW][2][4];
@@ -734,8 +733,8 @@ __global__ void __launch_bounds__(Q4Team<WIDE>::THREADS, 1) decode_q4_kernel(con
           uint32_t sc[2][2][GR / 2];  // scales of rows g and g + 8 of each tile
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            lds_scales<GR>(kb + at.ks[0] + i * tile_ks, sc[i][0]);
-            lds_scales<GR>(kb + at.ks[1] + i * tile_ks, sc[i][1]);
+            lds_scales<GR>(kb + at.ks + i * tile_ks, sc[i][0]);
+            lds_scales<GR>(kb + at.ks + i * tile_ks + 4 * GR, sc[i][1]);
           }
 #pragma unroll
           for (int i = 0; i < 2; ++i)
@@ -787,7 +786,8 @@ __global__ void __launch_bounds__(Q4Team<WIDE>::THREADS, 1) decode_q4_kernel(con
         // passes m + e_run or e_run changes.  So p <= 2^e_run always, the check
         // is one vote, and moves are rare once the first tokens have set it.
         float mx[NTW][2];
-        const bool big = ((chk.x | chk.y) & 0x40004000u) != 0 && e_run > 0.f;
+        const bool big =
+            ((so[0].x | so[0].y | so[1].x | so[1].y) & 0x40004000u) != 0 && e_run > 0.f;
         bool move = big;
 #pragma unroll
         for (int j = 0; j < NTW; ++j)
@@ -812,7 +812,7 @@ __global__ void __launch_bounds__(Q4Team<WIDE>::THREADS, 1) decode_q4_kernel(con
               n = (n > m_run[j][k] + e_old ? n + kQ4Head : m_run[j][k] + e_old) - e_run;
               const float al = exp2_approx(m_run[j][k] - n);
               m_run[j][k] = n;
-              l_run[j][k] *= al;
+              ov[j][k] *= al;  // the sum of weights
 #pragma unroll
               for (int mt = 0; mt < C::MT; ++mt) {
                 o[j][mt][k] *= al;
@@ -831,8 +831,6 @@ __global__ void __launch_bounds__(Q4Team<WIDE>::THREADS, 1) decode_q4_kernel(con
             const float p1 = exp2_approx(fmaf(s[j][i][1], fcol[j][1], -m_run[j][1]));
             const float p2 = exp2_approx(fmaf(s[j][i][2], fcol[j][0], -m_run[j][0]));
             const float p3 = exp2_approx(fmaf(s[j][i][3], fcol[j][1], -m_run[j][1]));
-            l_run[j][0] += p0 + p2;
-            l_run[j][1] += p1 + p3;
             b[j][i][0] = q4_movm(pack_f16(p0, p1));
             b[j][i][1] = q4_movm(pack_f16(p2, p3));
           }
@@ -846,9 +844,9 @@ __global__ void __launch_bounds__(Q4Team<WIDE>::THREADS, 1) decode_q4_kernel(con
           const uint32_t va = vb + at.vc;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const uint2 so = lds64(vb + at.vo + i * tile_vs);
+            const uint32_t a0 = (so[i].x & gm) | one, a2 = (so[i].y & gm) | one;
 #pragma unroll
-            for (int j = 0; j < NTW; ++j) q4_mma_rows8(ov[j], so.x, so.y, b[j][i][0], b[j][i][1]);
+            for (int j = 0; j < NTW; ++j) q4_mma_rows8(ov[j], a0, a2, b[j][i][0], b[j][i][1]);
           }
 #pragma unroll
           for (int q = 0; q < GR; ++q) {
@@ -895,12 +893,9 @@ __global__ void __launch_bounds__(Q4Team<WIDE>::THREADS, 1) decode_q4_kernel(con
     for (int j = 0; j < NTW; ++j)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1)
-          l_run[j][k] += __shfl_xor_sync(0xffffffffu, l_run[j][k], off);
-        if (g == 0) {
+        if (g == 4) {
           cmb_ml[((warp * NTW + j) * 8 + 2 * t + k) * 2] = m_run[j][k];
-          cmb_ml[((warp * NTW + j) * 8 + 2 * t + k) * 2 + 1] = l_run[j][k];
+          cmb_ml[((warp * NTW + j) * 8 + 2 * t + k) * 2 + 1] = ov[j][k];
         }
       }
     const long long slot_id = (long long)cta + p.seg;

@@ -8,7 +8,8 @@ the dequantized values.
 Tolerance of attention.  Weights are p = 2^(s - m + e) with the sum l, values
 v = c d (|c| <= 7, n = c + 8 <= 15).  The pass rounds p to fp16 (half a step:
 2^-11 relative) and p d again to fp16 (the same), multiplies the twice rounded
-product by n and the once rounded p by 8 d, in float32.  So the sum over T
+product by n and the once rounded p by 8 d, in float32; l sums the rounded p.  So
+the sum over T
 tokens is off by at most
     sum p d (2^-11 |c| + 2^-11 n)  <=  l (2^-11 + 2^-11 15 / 7) max|v|
                                    =  l 2^-10 1.572 max|v|
