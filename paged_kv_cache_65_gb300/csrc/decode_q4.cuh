@@ -238,6 +238,20 @@ __device__ __forceinline__ bool q4_wait_idle(uint64_t* bar, uint32_t parity) {
     __nanosleep(300);
   }
 }
+// named_bar_sync that tells every thread whether `ok` holds for all of them.
+__device__ __forceinline__ bool named_bar_all(int id, int n, bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.and.aligned.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"(id), "r"(n), "r"(static_cast<uint32_t>(ok))
+      : "memory");
+  return all != 0;
+}
+
 template <int D, bool WIDE>
 constexpr int decode_q4_team_bytes() {
   using C = Q4Cfg<D>;
@@ -559,7 +573,10 @@ __global__ void __launch_bounds__(Q4Team<WIDE>::THREADS, 1) decode_q4_kernel(con
       alive = false;
       if (lane == 0) record_status(a.status, 8);
     }
-    alive = __all_sync(0xffffffffu, alive);
+    // a wait that gave up ends the team as a whole, between pieces: its warps
+    // meet in barriers inside one
+    __syncwarp();
+    alive = named_bar_all(1 + team, kQ4Warps * 32, alive);
     if (!alive) return false;
     x = ring[di];
     __syncwarp();
