@@ -155,15 +155,6 @@ __device__ __forceinline__ void q4_mma(float (&d)[4], uint32_t a0, uint32_t a1, 
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// D += A . B for an A whose rows 8 .. 15 are zero: the upper half of D is not kept.
-__device__ __forceinline__ void q4_mma_rows8(float (&d)[2], uint32_t a0, uint32_t a2, uint32_t b0,
-                                             uint32_t b1) {
-  float z0, z1;
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%5}, "
-      "{%7,%8}, {%0,%1,%9,%9};"
-      : "+f"(d[0]), "+f"(d[1]), "=f"(z0), "=f"(z1)
-      : "r"(a0), "r"(0u), "r"(a2), "r"(b0), "r"(b1), "f"(0.f));
-}
 // Bytes 1 and 3 of a word as halves: the fp16 operands 16 n' + n of them.
 __device__ __forceinline__ uint32_t q4_odd_bytes(uint32_t w) { return __byte_perm(w, 0, 0x4341); }
 // without an addend: D = A . B
@@ -682,9 +673,9 @@ __global__ void __launch_bounds__(Q4Team<WIDE>::THREADS, 1) decode_q4_kernel(con
     // apart over a long piece the two would cancel to a small rest of large sums
     // (1.8x the error at 32,771 tokens).
     const uint32_t one = g == 4 ? 0x3c003c00u : 0u, gm = g < 4 ? 0xffffffffu : 0u;
-    float ov[NTW][2];
+    float ov[NTW][4];  // rows 8 .. 15, the upper half, repeat and are not used
 #pragma unroll
-    for (int j = 0; j < NTW; ++j) ov[j][0] = ov[j][1] = 0.f;
+    for (int j = 0; j < NTW; ++j) ov[j][0] = ov[j][1] = ov[j][2] = ov[j][3] = 0.f;
     auto fold = [&]() {
 #pragma unroll
       for (int j = 0; j < NTW; ++j)
@@ -863,7 +854,7 @@ __global__ void __launch_bounds__(Q4Team<WIDE>::THREADS, 1) decode_q4_kernel(con
           for (int i = 0; i < 2; ++i) {
             const uint32_t a0 = (so[i].x & gm) | one, a2 = (so[i].y & gm) | one;
 #pragma unroll
-            for (int j = 0; j < NTW; ++j) q4_mma_rows8(ov[j], a0, a2, b[j][i][0], b[j][i][1]);
+            for (int j = 0; j < NTW; ++j) q4_mma(ov[j], a0, a0, a2, a2, b[j][i][0], b[j][i][1]);
           }
 #pragma unroll
           for (int q = 0; q < GR; ++q) {
