@@ -29,6 +29,9 @@
  *     launch; they report launch errors only.  Bad block ids or slots met on
  *     the device are skipped and recorded in the pool's device status word;
  *     kv_pool_device_status() reads it.
+ *   - A pool belongs to the device that was current at its first device call;
+ *     q4_0 pools, gather_cached_rows and paged_tables_* refuse calls under
+ *     another current device (KV_ERR_INVALID_ARG).
  *   - The library allocates no device memory.  Device buffers (pools, the
  *     status word, decode workspaces) come from the caller.
  *   - A freed block may be handed out again by the next allocation; device

@@ -53,7 +53,7 @@
 // Wide form (up to 32 columns, two teams an SM): instruction issue.  A pass of
 // 32 tokens by 16 columns is 72 MMAs and about 420 other instructions, 1,250
 // cycles with two warps a scheduler, the tensor pipe busy 46% of them.  12
-// prefixes of 32,771 tokens by 32 columns: 214 us; with one n-tile a warp (the
+// prefixes of 32,771 tokens by 32 columns: 209 us; with one n-tile a warp (the
 // narrow form, unpacking everything four times) 298 us, with K and V converted
 // to fp16 for tcgen05 (tensor and shared memory traffic for every value, roles
 // waiting for one another) 276 us.

@@ -90,7 +90,8 @@ DecodeKernel decode_kernel(const kvPool* p) {
 
 // First device use of a pool: device, SM count, TMA descriptors.
 kvStatus ensure_device(kvPool* p) {
-  if (p->dev_ready) return KV_OK;
+  if (p->dev_ready)
+    return p->dtype != KV_DTYPE_Q4_0 || pool_on_current_device(p) ? KV_OK : KV_ERR_INVALID_ARG;
   if (!p->k || !p->v) return KV_ERR_INVALID_ARG;
   if (cudaGetDevice(&p->device) != cudaSuccess) return KV_ERR_CUDA;
   if (cudaDeviceGetAttribute(&p->sm_count, cudaDevAttrMultiProcessorCount, p->device) !=
@@ -765,6 +766,12 @@ int pool_sm_count(const kvPool* p) {
   return n;
 }
 
+// Whether the current device is the one of the pool's first device call.
+bool pool_on_current_device(const kvPool* p) {
+  int dev = 0;
+  return !p->dev_ready || (cudaGetDevice(&dev) == cudaSuccess && dev == p->device);
+}
+
 extern "C" {
 
 kvStatus kv_pool_device_status(kvPool* p, void* stream, int* out_bits) {
@@ -873,6 +880,7 @@ kvStatus gather_cached_rows(kvPool* p, int layer, const int64_t* d_slots, int n_
     return KV_ERR_INVALID_ARG;
   kvStatus s = ensure_device(p);
   if (s != KV_OK) return s;
+  if (!pool_on_current_device(p)) return KV_ERR_INVALID_ARG;
   const cudaError_t e = pkv::launch_gather_rows(p, layer, d_slots, n_tokens, d_k_out, d_v_out,
                                                 out_dtype, as_stream(stream));
   return e == cudaSuccess ? KV_OK : KV_ERR_CUDA;

@@ -146,6 +146,7 @@ constexpr int kMaxDecodeCtas = 1024;
 
 // SM count of the pool's device, 0 while unknown (device.cu).
 int pool_sm_count(const kvPool* p);
+bool pool_on_current_device(const kvPool* p);
 
 // Workspace bytes of a planned decode pass (plan.cpp).
 size_t plan_workspace_bytes(int n_segs, int c_max, int D);

@@ -310,6 +310,7 @@ kvStatus check_tables(const kvPool* p, const kvTables* t, const int32_t* d_rows,
   if (static_cast<int64_t>(t->max_blocks) * p->B >= (int64_t(1) << 31)) return KV_ERR_INVALID_ARG;
   if (!t->tables || !t->lens || !t->free_ids || !t->free_state) return KV_ERR_INVALID_ARG;
   if (!d_rows && n_seq > t->n_rows) return KV_ERR_INVALID_ARG;
+  if (!pool_on_current_device(p)) return KV_ERR_INVALID_ARG;
   if (n_seq > 0 && (!ws || (reinterpret_cast<uintptr_t>(ws) & 15) != 0 ||
                     ws_bytes < workspace_bytes(n_seq)))
     return KV_ERR_INVALID_ARG;
