@@ -82,7 +82,9 @@ struct DecodeArgs {
   // q8_0 pools: the fp16 scales [L][N][H_kv][B][D / 32] of K and V
   const void* k_sc = nullptr;
   const void* v_sc = nullptr;
-  // q4_0 pass: tables and lengths are read only after the previous grid
+  // q4_0 pass: least chunk of a plan; tables and lengths are read only after the
+  // previous grid
+  long long min_chunk = 1;
   bool meta_wait = false;
 };
 
@@ -194,6 +196,8 @@ __device__ __forceinline__ int seq_blocks(const int32_t* ctx, int s, int B, int 
 }
 
 // One warp: total W, chunk, and the sequence containing block index r0.
+// MINC: with q4_min_blocks' lower bound on the chunk.
+template <bool MINC = false>
 __device__ inline WalkStart find_start(const int32_t* ctx, int n_seq, int B, int H, int max_blocks,
                                        int grid, int cta, int32_t* status) {
   const int lane = threadIdx.x & 31;
@@ -210,6 +214,10 @@ __device__ inline WalkStart find_start(const int32_t* ctx, int n_seq, int B, int
   w.W = run;
   w.chunk = (run + grid - 1) / grid;
   if (w.chunk == 0) w.chunk = 1;
+  if constexpr (MINC) {
+    const int least = q4_min_blocks(static_cast<float>(run) / static_cast<float>(n_seq * H), B);
+    if (w.chunk < least) w.chunk = least;
+  }
   const long long r0 = (long long)cta * w.chunk;
   w.s = n_seq;
   w.pre = run;

@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(Q4Team<WIDE>::THREADS, 1) decode_q4_kernel(con
     if constexpr (PLAN) {
       const long long W = a.plan_W;
       long long chunk = (W + a.grid - 1) / a.grid;
-      if (chunk == 0) chunk = 1;
+      if (chunk < a.min_chunk) chunk = a.min_chunk;
       const long long r0 = (long long)cta * chunk;
       plw.segs = a.segs;
       plw.n_segs = a.n_segs;
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(Q4Team<WIDE>::THREADS, 1) decode_q4_kernel(con
       plw.s = 0;
       if (!use_rec) plw.s = r0 < W ? plan_find(a.segs, a.n_segs, r0) : a.n_segs;
     } else {
-      const WalkStart w = find_start(a.ctx, a.n_seq, B, H, a.max_blocks, a.grid, cta, a.status);
+      const WalkStart w = find_start<true>(a.ctx, a.n_seq, B, H, a.max_blocks, a.grid, cta, a.status);
       const long long r0 = (long long)cta * w.chunk;
       pw.ctx = a.ctx;
       pw.n_seq = a.n_seq;

@@ -403,8 +403,8 @@ template <int D>
 __global__ void __launch_bounds__(128) merge_kernel(const long long* __restrict__ pre,
                                                     const float* __restrict__ ws_ml,
                                                     const float* __restrict__ ws_o, int n_seq,
-                                                    int H, int Hq, int grid, float* out_f32,
-                                                    __nv_bfloat16* out_bf16) {
+                                                    int H, int Hq, int grid, int min_b,
+                                                    float* out_f32, __nv_bfloat16* out_bf16) {
   pkv::griddep_wait();
   pkv::griddep_launch_dependents();
   constexpr int DL = D / 32;
@@ -416,6 +416,10 @@ __global__ void __launch_bounds__(128) merge_kernel(const long long* __restrict_
   const long long W = pre[n_seq];
   long long chunk = (W + grid - 1) / grid;
   if (chunk == 0) chunk = 1;
+  if (min_b > 0) {  // a q4_0 pool's split, blocks of min_b tokens
+    const int least = q4_min_blocks(static_cast<float>(W) / static_cast<float>(n_seq * H), min_b);
+    if (chunk < least) chunk = least;
+  }
   {
     const int hq = blockIdx.y * 4 + warp;
     if (hq >= Hq) return;
@@ -499,7 +503,7 @@ constexpr int kMergePlanWarps = 4;
 template <int D, int PRE>
 __global__ void __launch_bounds__(kMergePlanWarps * 32) merge_plan_kernel(
     const PlanSeg* __restrict__ segs, const int32_t* __restrict__ eoff,
-    const PlanEntry* __restrict__ ents, long long W, int grid, int c_max,
+    const PlanEntry* __restrict__ ents, long long W, int grid, long long min_chunk, int c_max,
     const float* __restrict__ ws_ml, const float* __restrict__ ws_o, int H, int Hq,
     float* out_f32, __nv_bfloat16* out_bf16) {
   constexpr int DL = D / 32;
@@ -510,7 +514,7 @@ __global__ void __launch_bounds__(kMergePlanWarps * 32) merge_plan_kernel(
   const int G = Hq / H;
   const int h = live ? hq / G : 0, g = live ? hq - h * G : 0;
   long long chunk = (W + grid - 1) / grid;
-  if (chunk == 0) chunk = 1;
+  if (chunk < min_chunk) chunk = min_chunk;
   const int e0 = live ? eoff[s * H + h] : 0, e1 = live ? eoff[s * H + h + 1] : 0;
   // workspace slot of the k-th piece over the entries, or -1 past the last
   auto piece_slot = [&](int k) -> int {
@@ -1010,13 +1014,14 @@ kvStatus paged_decode_merge(kvPool* p, int n_q_heads, const int32_t* d_context_l
   float* of = out_dtype == KV_DTYPE_F32 ? reinterpret_cast<float*>(d_out) : nullptr;
   __nv_bfloat16* ob = out_dtype == KV_DTYPE_BF16 ? reinterpret_cast<__nv_bfloat16*>(d_out) : nullptr;
   const dim3 mg(n_seq, (n_q_heads + 3) / 4);
+  const int min_b = p->dtype == KV_DTYPE_Q4_0 ? p->B : 0;
   const cudaError_t e =
       p->D == 128 ? pkv::launch_kernel(p->pdl, merge_kernel<128>, mg, dim3(128), 0,
                                        as_stream(stream), pre, ml, o, n_seq, p->H, n_q_heads,
-                                       grid, of, ob)
+                                       grid, min_b, of, ob)
                   : pkv::launch_kernel(p->pdl, merge_kernel<64>, mg, dim3(128), 0,
                                        as_stream(stream), pre, ml, o, n_seq, p->H, n_q_heads,
-                                       grid, of, ob);
+                                       grid, min_b, of, ob);
   return e == cudaSuccess ? KV_OK : KV_ERR_CUDA;
 }
 
@@ -1110,6 +1115,7 @@ kvStatus partials_planned(kvPool* p, int layer, const void* d_q, int n_q_heads,
   a.n_segs = hd.n_segs;
   a.c_max = hd.c_max;
   a.plan_W = hd.W;
+  a.min_chunk = plan_min_chunk(p, hd);
   a.starts = hd.start_grid > 0 ? reinterpret_cast<const PlanStart*>(dp + hd.start_off) : nullptr;
   a.start_grid = hd.start_grid;
   a.k_new = d_k_new;
@@ -1198,6 +1204,7 @@ kvStatus paged_decode_merge_planned(kvPool* p, int n_q_heads, const void* d_plan
   __nv_bfloat16* ob = out_dtype == KV_DTYPE_BF16 ? reinterpret_cast<__nv_bfloat16*>(d_out) : nullptr;
   const dim3 mg(hd.n_seq, (n_q_heads + kMergePlanWarps - 1) / kMergePlanWarps);
   const int gr = grid > 0 ? grid : 1;
+  const long long least = plan_min_chunk(p, hd);
   const dim3 mb(kMergePlanWarps * 32);
   cudaError_t e = cudaSuccess;
   if (p->merge_deep_ctas < 0) {  // resident CTAs of the deeper variant, once per pool
@@ -1212,7 +1219,7 @@ kvStatus paged_decode_merge_planned(kvPool* p, int n_q_heads, const void* d_plan
   const bool deep = static_cast<long long>(mg.x) * mg.y <= p->merge_deep_ctas;
   auto go = [&](auto kern) {
     return pkv::launch_kernel(p->pdl, kern, mg, mb, 0, as_stream(stream), segs, eoff, ents, hd.W,
-                              gr, hd.c_max, ml, o, p->H, n_q_heads, of, ob);
+                              gr, least, hd.c_max, ml, o, p->H, n_q_heads, of, ob);
   };
   if (p->D == 128)
     e = deep ? go(merge_plan_kernel<128, 12>) : go(merge_plan_kernel<128, 8>);

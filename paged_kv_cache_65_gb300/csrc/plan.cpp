@@ -80,10 +80,10 @@ int plan_grid(const kvPool* p, int kernel, int G) {
 // ceil(W / grid) (at least 1); its walk starts at the last segment whose
 // first unit is at or before c * chunk and yields the pieces PlanWalker::next
 // does.
-void plan_starts(const std::vector<PlanSeg>& segs, int64_t W, int grid, int B,
+void plan_starts(const std::vector<PlanSeg>& segs, int64_t W, int grid, int64_t min_chunk, int B,
                  const std::vector<const kvSeq*>& seqs, PlanStart* out) {
   int64_t chunk = (W + grid - 1) / grid;
-  if (chunk == 0) chunk = 1;
+  if (chunk < min_chunk) chunk = min_chunk;
   const int n = static_cast<int>(segs.size());
   int lo = 0;  // last segment with wpre <= r0; r0 grows with c, so lo only moves on
   for (int c = 0; c < grid; ++c) {
@@ -136,6 +136,16 @@ struct PlanScratch {
 thread_local PlanScratch t_scratch;
 
 }  // namespace
+
+long long plan_min_chunk(const kvPool* p, const PlanHeader& hd) {
+  if (p->dtype != KV_DTYPE_Q4_0) return 1;
+  // a plan for the wide form holds most of its work in the shared segments
+  const bool shared = hd.kernel == kPlanKernelTc && hd.n_shared_segs > 0;
+  const int n = shared ? hd.n_shared_segs : hd.n_segs, w = plan_block_weight(8, hd.kernel);
+  return n > 0 ? static_cast<long long>(w) *
+                     q4_min_blocks(static_cast<float>(hd.W / w) / static_cast<float>(n), p->B)
+               : 1;
+}
 
 size_t plan_workspace_bytes(int n_segs, int c_max, int D) {
   const size_t n_slots = static_cast<size_t>(kMaxDecodeCtas) + static_cast<size_t>(n_segs);
@@ -459,7 +469,7 @@ kvStatus plan_build(const kvPool* p, const int32_t* seq_ids, int n_seq, int n_q_
   hd.start_grid = grid;
   std::memcpy(out, &hd, sizeof(hd));
   if (grid > 0)
-    plan_starts(segs, W, grid, B, seqs, reinterpret_cast<PlanStart*>(out + l.start));
+    plan_starts(segs, W, grid, plan_min_chunk(p, hd), B, seqs, reinterpret_cast<PlanStart*>(out + l.start));
   if (!segs.empty()) std::memcpy(out + l.seg, segs.data(), sizeof(PlanSeg) * segs.size());
   if (!members.empty()) std::memcpy(out + l.mem, members.data(), sizeof(int32_t) * members.size());
   int32_t* eoff = reinterpret_cast<int32_t*>(out + l.eoff);

@@ -16,6 +16,7 @@
 // segment are wpre / chunk .. (wpre + len*w - 1) / chunk.
 #pragma once
 
+#include <cmath>
 #include <cstdint>
 
 struct PlanHeader {
@@ -112,6 +113,26 @@ constexpr int plan_piece_units(int kernel) {
   return kernel == kPlanKernelTc ? 32 * plan_block_weight(8, kernel)
                                  : 4 * plan_block_weight(8, kernel);
 }
+// q4_0 pools: the fewest blocks a team of the split takes, for segments of
+// `blocks` blocks of B tokens on average.  A team's time goes in stages of 128
+// tokens, about 1.1 us each, and the merge pass reads a segment's pieces eight at
+// a time, about 0.7 us each, so a segment of N tokens is best cut into pieces of
+// sqrt(N * 128 / 8 * 0.7 / 1.1), about sqrt(10 N); but a team that ends one segment
+// and begins the next takes two pieces one after the other, 2 to 3 us, which up
+// to 32 pieces cost less.  Where there is enough work for every team the chunk is
+// larger anyway.  Without and with it: six branches of 300 tokens (whose units,
+// finer than blocks, made empty pieces) 30 and 8 us, two sequences of 25,000
+// tokens and one K/V head 26 and 19, one of 131,071 46 and 28, one of 8,191 and
+// eight heads 17 and 12.
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+inline int q4_min_blocks(float blocks, int B) {
+  if (blocks < 64.f) return 1;  // the bound below
+  const float best = sqrtf(10.f * blocks / static_cast<float>(B));
+  return static_cast<int>(best < blocks * 0.03125f ? best : blocks * 0.03125f);
+}
+
 // Units per block of a segment of n_blocks blocks.
 constexpr int plan_seg_weight(int ncols, int kernel, int n_blocks) {
   return plan_block_weight(ncols, kernel) +

@@ -148,6 +148,10 @@ constexpr int kMaxDecodeCtas = 1024;
 int pool_sm_count(const kvPool* p);
 bool pool_on_current_device(const kvPool* p);
 
+// Fewest work units of a CTA of the planned split (plan.cpp).
+struct PlanHeader;
+long long plan_min_chunk(const kvPool* p, const PlanHeader& hd);
+
 // Workspace bytes of a planned decode pass (plan.cpp).
 size_t plan_workspace_bytes(int n_segs, int c_max, int D);
 
