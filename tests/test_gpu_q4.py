@@ -437,6 +437,23 @@ def test_v_scales_that_grow_and_shrink_along_a_sequence(low, high, at, path, D, 
     assert c.kv_pool_device_status() == 0
 
 
+@pytest.mark.parametrize("planned,path", [(False, MMA), (True, MMA), (True, WIDE)])
+@pytest.mark.parametrize("G,B,D", [(8, 8, 128), (4, 16, 64), (1, 64, 128)])
+def test_few_long_segments_of_one_head(G, B, D, planned, path):
+    # less work than teams over long segments: the split takes its least chunk,
+    # and short sequences share chunks with the long ones
+    wl = q4_workload("q4_least", G, B, 47, [9001, 3, 2500, 64], H=1, D=D, fork=6007)
+    orc = OracleRun(wl)
+    cache, run = make(wl, path=path)
+    for step in range(2):  # the second plan's start records know the launch
+        so, co, q, outs = orc.step(step)
+        _, k, v = wl.step_values(step)
+        sg, _, og = run.step(wl.decode_seqs, q, k, v, planned=planned)
+        assert list(sg) == so
+        assert max_err(og.cpu().numpy()[0], outs[0]) <= step_tol(orc, q)
+    assert cache.kv_pool_device_status() == 0
+
+
 @pytest.mark.parametrize("path", [MMA, WIDE])
 def test_long_context_and_offsets_past_32_bits(path):
     # a pool whose byte offsets pass 2^32 and one sequence through its last blocks
