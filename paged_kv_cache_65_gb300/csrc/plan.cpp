@@ -77,7 +77,7 @@ int plan_grid(const kvPool* p, int kernel, int G) {
 
 // Start records for `grid` CTAs, following the device's split exactly: CTA c
 // takes the work units [c * chunk, min((c + 1) * chunk, W)), chunk =
-// ceil(W / grid) (at least 1); its walk starts at the last segment whose
+// ceil(W / grid) (at least min_chunk); its walk starts at the last segment whose
 // first unit is at or before c * chunk and yields the pieces PlanWalker::next
 // does.
 void plan_starts(const std::vector<PlanSeg>& segs, int64_t W, int grid, int64_t min_chunk, int B,
