@@ -46,8 +46,8 @@
 // SM): memory.  A longer context adds time at 6.8 TB/s of codes and scales (a
 // pass that only copies: 7.0), and what is left of a call is its start, the
 // pieces' ends and the merge pass, 8.6 us at 333 tokens.  37 sequences of 2K
-// tokens, 8 K/V heads of 4 query heads: 26.7 us, 24 without any arithmetic;
-// 131,071 tokens, 8 heads of 8: 39.5 us, 36 without arithmetic.  It took 30 and 43
+// tokens, 8 K/V heads of 4 query heads: 27.0 us, 24 without any arithmetic;
+// 131,071 tokens, 8 heads of 8: 39.6 us, 36 without arithmetic.  It took 30 and 43
 // us with CTAs of 5 warps instead of teams: 128 registers a thread spilled, and
 // the compiler could not overlap the tile's chains.
 // Wide form (up to 32 columns, two teams an SM): instruction issue.  A pass of
